@@ -433,6 +433,139 @@ imem_status imem_decode_online(imem_ctx* ctx, int batch, int B, const void* x_ne
                                int32_t* cache_len, int cap, float* M, float* bstab, void* out,
                                int32_t* evicted, void* workspace, void* stream);
 
+/* ---- rotary positions and the paged cache --------------------------------
+ *
+ * The path above takes a prompt's rotated K and V as given, in one contiguous
+ * array. The calls below produce them in a serving loop: a chunk of new tokens
+ * is rotated and written into a paged cache, attends over it, and the rows
+ * that stay or leave are gathered out of the pages into the contiguous arrays
+ * that imem_decode and imem_update_memory read. (No counterpart in the paper:
+ * rotary positions, paged caches and causal attention are the frozen model's.)
+ *
+ * They use the context's n_q_heads, n_kv_heads, head_dim and dtype, need no
+ * workspace, launch nothing for zero tokens, and can be captured in a graph
+ * (no set-up of theirs may run during the capture: call each once before).
+ *
+ * Tokens. The new tokens of all sequences are packed along one axis of
+ * n_tokens rows: tok_start [batch + 1] int32 (device, ascending, tok_start[0]
+ * >= 0, tok_start[batch] <= n_tokens): sequence s has tokens [tok_start[s],
+ * tok_start[s + 1]), possibly none. tok_start = NULL: n_tokens / batch each
+ * (n_tokens must be a multiple of batch). Rows outside every sequence are
+ * padding: neither read for a result nor written.
+ * Rows of a token tensor are `stride` elements apart (0: heads * head_dim),
+ * the heads of one row contiguous; a stride must keep rows 16-byte aligned
+ * and apart, so slices of a joint QKV projection can be passed as they are.
+ *
+ * Cache. k, v [n_pages, page_size, Hkv, d] (model dtype), page_size a power of
+ * two from 16 to 1024; block_table [batch, max_pages] int32: the page of each
+ * page_size tokens of a sequence; kv_len [batch] int32: cached tokens of a
+ * sequence INCLUDING the new tokens of the call, so the i-th of a sequence's n
+ * new tokens has position kv_len[s] - n + i. A negative position (a sequence
+ * padded in front) is padding too: it is not appended and attends to nothing.
+ * Table entries past the last page that kv_len reaches are not read. A length
+ * above max_pages * page_size or an entry outside [0, n_pages) that a call
+ * needs is reported by imem_sync as IMEM_ERR_RANGE (nothing out of bounds is
+ * read or written; that sequence's results are unspecified). A tok_start that
+ * descends or leaves [0, n_tokens] is reported likewise, every result of the
+ * call is then unspecified. All tables and lengths are read on the device, in
+ * stream order. */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* block_table;
+  const int32_t* kv_len;
+  int n_pages, page_size, max_pages;
+} imem_paged;
+
+/* Which dimensions form a pair i of the first rot_dim: HALF (i, i + rot_dim/2),
+ * INTERLEAVED (2i, 2i + 1). */
+typedef enum { IMEM_ROPE_HALF = 0, IMEM_ROPE_INTERLEAVED = 1 } imem_rope_layout;
+
+/* Frequencies theta_i = base^(-2i/rot_dim), stretched for contexts longer than
+ * those of training: theta'_i = (w_i + (1 - w_i) / factor) theta_i with
+ *   PLAIN   w = 1
+ *   LINEAR  w = 0 (positions interpolated)
+ *   BAND    w = clamp((n_i - low) / (high - low), 0, 1), n_i = orig_len theta_i
+ *           / (2 pi) turns over the original context: pairs of fewer than `low`
+ *           turns are stretched, of more than `high` kept
+ *   RAMP    w = 1 - clamp((i - a) / max(b - a, 0.001), 0, 1) over the pair's index,
+ *           a = floor(x(high)), b = ceil(x(low)), both held in [0, rot_dim/2 - 1],
+ *           x(n) = rot_dim ln(orig_len / (2 pi n)) / (2 ln base) (YaRN's ramp) */
+typedef enum { IMEM_ROPE_PLAIN = 0, IMEM_ROPE_LINEAR = 1, IMEM_ROPE_BAND = 2,
+               IMEM_ROPE_RAMP = 3 } imem_rope_scaling;
+
+typedef struct {
+  int rot_dim;       /* rotated dimensions of a head: a multiple of 16, <= head_dim */
+  int layout;        /* imem_rope_layout                                            */
+  int scaling;       /* imem_rope_scaling                                           */
+  int orig_len;      /* BAND, RAMP: the original context length, >= 1               */
+  double base;       /* > 1                                                         */
+  double factor;     /* LINEAR, BAND, RAMP: >= 1                                    */
+  double low, high;  /* BAND, RAMP: turns, 0 < low < high                           */
+  double magnitude;  /* cos and sin are multiplied by it (1: a pure rotation), > 0  */
+} imem_rope;
+
+/* Sets the context's rotation (host only; captured graphs keep the one they
+ * were captured with). NULL: none, calls that rotate then return INVALID_ARG.
+ * The phase of position p is p * theta' / (2 pi) mod 1 in 64-bit fixed point,
+ * so far positions lose nothing. Errors: INVALID_ARG, UNSUPPORTED (rot_dim). */
+imem_status imem_set_rope(imem_ctx* ctx, const imem_rope* rope);
+
+/* Rotates queries q [n_tokens, Hq, d] and keys k [n_tokens, Hkv, d] (either may
+ * be NULL, with its output) by positions [n_tokens] (int32, device, any sign)
+ * into q_out, k_out (the same tensor is allowed, other overlaps are not).
+ * For a pair (x1, x2) and angle a = position * theta': magnitude * (x1 cos a -
+ * x2 sin a, x2 cos a + x1 sin a), computed in fp32 and rounded once;
+ * dimensions past rot_dim are copied. inverse = 1 rotates by -a: the
+ * gradient of the rotation, and its inverse where magnitude = 1.
+ * Errors: INVALID_ARG (also no rotation set, no tensor), SHAPE, ALIGN, CUDA. */
+imem_status imem_rotate(imem_ctx* ctx, int n_tokens, const int32_t* positions, const void* q,
+                        int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                        int64_t k_stride, void* k_out, int64_t k_out_stride, int inverse,
+                        void* stream);
+
+/* Writes the new tokens' keys (rotated if rotate = 1) and values into the
+ * cache at their positions and, if q is not NULL, their queries (rotated
+ * likewise) to q_out, which may be q: one launch. Angles are those of the cache
+ * positions, or of `positions` [n_tokens] (int32, device) if not NULL (for
+ * caches that no longer hold every token). Two sequences must not append to
+ * one page slot. Errors: INVALID_ARG, SHAPE, ALIGN, CUDA; RANGE via imem_sync. */
+imem_status imem_append_paged(imem_ctx* ctx, int batch, int n_tokens, const int32_t* tok_start,
+                              const int32_t* positions, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                              void* q_out, int64_t q_out_stride, int rotate,
+                              const imem_paged* cache, void* stream);
+
+/* Causal attention of the new tokens over the paged cache (their own rows
+ * already appended). Query head h uses KV head h/(Hq/Hkv); for a token at position p
+ *   s_j = scale q . k_j, out = sum_{j <= p} softmax(s)_j v_j     (out model dtype)
+ *   lse = ln sum_{j <= p} exp(s_j)            (fp32 [n_tokens, Hq], or NULL)
+ * A token that sees no key (p < 0) gets out = 0 and lse = -inf. Keys and values
+ * past kv_len are never used, whatever the pages hold there. Within a chunk a
+ * value row that is not finite may also reach the outputs of the up to 127
+ * tokens before it. softmax in fp32; bf16: probabilities are rounded to bf16
+ * for the product with V, as imem_decode does.
+ * scale > 0 and finite; 0: 1/sqrt(d).
+ * max_new: no sequence has more new tokens (<= n_tokens; one that has more is
+ * reported as RANGE and its tokens past max_new are not computed). max_len: the
+ * longest kv_len expected (a hint for splitting the work; results do not
+ * depend on it beyond the order of fp32 sums).
+ * Errors: INVALID_ARG, SHAPE, ALIGN, CUDA; RANGE, TIMEOUT via imem_sync. */
+imem_status imem_attend_paged(imem_ctx* ctx, int batch, int n_tokens, const int32_t* tok_start,
+                              int max_new, int max_len, const void* q, int64_t q_stride,
+                              const imem_paged* cache, float scale, void* out, int64_t out_stride,
+                              float* lse, void* stream);
+
+/* Copies rows of the paged cache to contiguous arrays: K, V [batch, cap, Hkv, d],
+ * K[s, i] = cached key at position idx[s * idx_stride + i], 0 <= i < n (n <= cap;
+ * rows from n on are not written). idx = NULL: positions 0..n-1, those at or
+ * past kv_len[s] skipped. An index outside [0, kv_len[s]) is reported as RANGE
+ * and its row not written. After gathering into a retained cache that decode
+ * steps have used, call imem_decode_invalidate.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, CUDA; RANGE via imem_sync. */
+imem_status imem_gather_paged(imem_ctx* ctx, int batch, int n, const int32_t* idx, int idx_stride,
+                              const imem_paged* cache, void* K, void* V, int cap, void* stream);
+
 /* Failure-path self-test (no counterpart in the papers): launches one CTA
  * that waits on a transaction barrier nothing completes, through the same
  * bounded wait every kernel of this library uses, with the given limit in SM

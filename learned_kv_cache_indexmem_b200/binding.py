@@ -20,6 +20,8 @@ STATUS = {0: "IMEM_OK", 1: "IMEM_ERR_INVALID_ARG", 2: "IMEM_ERR_SHAPE", 3: "IMEM
           7: "IMEM_ERR_RANGE"}
 FP32, BF16 = 0, 1
 READOUT_GATED, READOUT_MOMENT = 0, 1
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "band": 2, "ramp": 3}
 
 
 class IndexMemError(RuntimeError):
@@ -42,6 +44,19 @@ class Weights(ctypes.Structure):
     _fields_ = [("W_idx_q", ctypes.c_void_p), ("W_idx_k", ctypes.c_void_p),
                 ("w_idx_g", ctypes.c_void_p), ("W_phi", ctypes.c_void_p),
                 ("w_gate", ctypes.c_void_p)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("orig_len", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 _lib = None
@@ -105,6 +120,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.imem_indexer_score.argtypes = [vp, i, i, vp, i, i, vp, vp]
     lib.imem_select_compact.restype = i
     lib.imem_select_compact.argtypes = [vp, i, i, i, vp, vp, vp, vp, vp, vp, vp, i, vp, vp]
+    pp, i64 = ctypes.POINTER(Paged), ctypes.c_int64
+    lib.imem_set_rope.restype = i
+    lib.imem_set_rope.argtypes = [vp, ctypes.POINTER(Rope)]
+    lib.imem_rotate.restype = i
+    lib.imem_rotate.argtypes = [vp, i, vp, vp, i64, vp, i64, vp, i64, vp, i64, i, vp]
+    lib.imem_append_paged.restype = i
+    lib.imem_append_paged.argtypes = [vp, i, i, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, i, pp,
+                                      vp]
+    lib.imem_attend_paged.restype = i
+    lib.imem_attend_paged.argtypes = [vp, i, i, vp, i, i, vp, i64, pp, f, vp, i64, vp, vp]
+    lib.imem_gather_paged.restype = i
+    lib.imem_gather_paged.argtypes = [vp, i, i, vp, i, pp, vp, vp, i, vp]
     _lib = lib
     return lib
 
@@ -288,3 +315,40 @@ def join(ctx, stream=None) -> None:
 
 def sync(ctx, stream=None) -> None:
     _check(load().imem_sync(ctx, _stream(stream)), "imem_sync")
+
+
+def set_rope(ctx, rope: Optional[Rope]) -> None:
+    _check(load().imem_set_rope(ctx, ctypes.byref(rope) if rope is not None else None),
+           "imem_set_rope")
+
+
+def make_paged(k, v, block_table, kv_len, n_pages, page_size, max_pages) -> Paged:
+    return Paged(_ptr(k), _ptr(v), _ptr(block_table), _ptr(kv_len), n_pages, page_size, max_pages)
+
+
+def rotate(ctx, n_tokens, positions, q, q_stride, q_out, q_out_stride, k, k_stride, k_out,
+           k_out_stride, inverse=False, stream=None):
+    _check(load().imem_rotate(
+        ctx, n_tokens, _ptr(positions), _ptr(q), q_stride, _ptr(q_out), q_out_stride, _ptr(k),
+        k_stride, _ptr(k_out), k_out_stride, int(inverse), _stream(stream)), "imem_rotate")
+
+
+def append_paged(ctx, batch, n_tokens, tok_start, positions, k, k_stride, v, v_stride, q, q_stride,
+                 q_out, q_out_stride, rotate, cache: Paged, stream=None):
+    _check(load().imem_append_paged(
+        ctx, batch, n_tokens, _ptr(tok_start), _ptr(positions), _ptr(k), k_stride, _ptr(v),
+        v_stride, _ptr(q), q_stride, _ptr(q_out), q_out_stride, int(rotate), cache,
+        _stream(stream)), "imem_append_paged")
+
+
+def attend_paged(ctx, batch, n_tokens, tok_start, max_new, max_len, q, q_stride, cache: Paged,
+                 scale, out, out_stride, lse, stream=None):
+    _check(load().imem_attend_paged(
+        ctx, batch, n_tokens, _ptr(tok_start), max_new, max_len, _ptr(q), q_stride, cache, scale,
+        _ptr(out), out_stride, _ptr(lse), _stream(stream)), "imem_attend_paged")
+
+
+def gather_paged(ctx, batch, n, idx, idx_stride, cache: Paged, K, V, cap, stream=None):
+    _check(load().imem_gather_paged(
+        ctx, batch, n, _ptr(idx), idx_stride, cache, _ptr(K), _ptr(V), cap, _stream(stream)),
+        "imem_gather_paged")

@@ -742,6 +742,216 @@ imem_status imem_decode_online(imem_ctx* h, int batch, int B, const void* x_new,
                                                      (int*)(wsb + ws.dec_tag_off), st));
 }
 
+namespace {
+// A token tensor's stride in elements: 0 stands for `heads` contiguous heads;
+// rows must stay 16-byte aligned and apart.
+imem_status check_stride(const Ctx& c, int64_t* stride, int heads) {
+  const int64_t row = (int64_t)heads * c.cfg.head_dim;
+  if (*stride == 0) *stride = row;
+  if (*stride < row) return IMEM_ERR_SHAPE;
+  const int64_t esize = c.cfg.dtype == IMEM_BF16 ? 2 : 4;
+  return (*stride * esize) % 16 ? IMEM_ERR_ALIGN : IMEM_OK;
+}
+
+// The 2^32 tokens' worth of grid and index arithmetic the kernels are written
+// for: batch and KV heads are grid dimensions, tokens * group stays an int.
+imem_status check_tokens(const Ctx& c, int batch, int n_tokens, const int32_t* tok_start) {
+  if (batch < 1 || batch > 65535 || c.cfg.n_kv_heads > 65535) return IMEM_ERR_SHAPE;
+  if (n_tokens < 0 || n_tokens > (1 << 24)) return IMEM_ERR_SHAPE;
+  if (!tok_start) return n_tokens % batch ? IMEM_ERR_SHAPE : IMEM_OK;
+  return aligned16(tok_start) ? IMEM_OK : IMEM_ERR_ALIGN;
+}
+
+imem_status check_paged(const imem_paged* p, imem::PagedView* v) {
+  if (!p) return IMEM_ERR_INVALID_ARG;
+  IMEM_CHECK(check_ptr(p->k));
+  IMEM_CHECK(check_ptr(p->v));
+  IMEM_CHECK(check_ptr(p->block_table));
+  IMEM_CHECK(check_ptr(p->kv_len));
+  if (p->n_pages < 1 || p->max_pages < 1) return IMEM_ERR_SHAPE;
+  int log = 0;
+  while (log < 10 && (1 << log) < p->page_size) ++log;
+  if (p->page_size < 16 || (1 << log) != p->page_size) return IMEM_ERR_UNSUPPORTED;
+  if ((int64_t)p->n_pages << log > INT32_MAX) return IMEM_ERR_SHAPE;
+  v->k = p->k;
+  v->v = p->v;
+  v->table = p->block_table;
+  v->len = p->kv_len;
+  v->n_pages = p->n_pages;
+  v->page_log = log;
+  v->max_pages = p->max_pages;
+  return IMEM_OK;
+}
+}  // namespace
+
+imem_status imem_set_rope(imem_ctx* h, const imem_rope* r) {
+  if (!h) return IMEM_ERR_INVALID_ARG;
+  imem::RopeTable& t = h->c.rope;
+  if (!r) {
+    t.rot_dim = 0;
+    return IMEM_OK;
+  }
+  if (r->layout != IMEM_ROPE_HALF && r->layout != IMEM_ROPE_INTERLEAVED) return IMEM_ERR_INVALID_ARG;
+  if (r->scaling < IMEM_ROPE_PLAIN || r->scaling > IMEM_ROPE_RAMP) return IMEM_ERR_INVALID_ARG;
+  if (!(r->base > 1) || isinf(r->base) || !(r->magnitude > 0) || isinf(r->magnitude))
+    return IMEM_ERR_INVALID_ARG;
+  const bool ramps = r->scaling == IMEM_ROPE_BAND || r->scaling == IMEM_ROPE_RAMP;
+  if (r->scaling != IMEM_ROPE_PLAIN && (!(r->factor >= 1) || isinf(r->factor)))
+    return IMEM_ERR_INVALID_ARG;
+  if (ramps && (r->orig_len < 1 || !(r->low > 0) || !(r->high > r->low) || isinf(r->high)))
+    return IMEM_ERR_INVALID_ARG;
+  if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > h->c.cfg.head_dim)
+    return IMEM_ERR_UNSUPPORTED;
+  const double tau = 6.283185307179586476925;
+  const int half = r->rot_dim / 2;
+  const auto at = [&](double turns) {
+    return r->rot_dim * log(r->orig_len / (tau * turns)) / (2 * log(r->base));
+  };
+  const auto hold = [&](double x) { return fmin(fmax(x, 0.0), half - 1.0); };
+  for (int i = 0; i < half; ++i) {
+    const double theta = pow(r->base, -2.0 * i / r->rot_dim);
+    double keep = 1.0;
+    if (r->scaling == IMEM_ROPE_LINEAR) keep = 0.0;
+    if (r->scaling == IMEM_ROPE_BAND)
+      keep = fmin(fmax((r->orig_len * theta / tau - r->low) / (r->high - r->low), 0.0), 1.0);
+    if (r->scaling == IMEM_ROPE_RAMP) {
+      const double a = hold(floor(at(r->high))), b = hold(ceil(at(r->low)));
+      keep = 1.0 - fmin(fmax((i - a) / fmax(b - a, 1e-3), 0.0), 1.0);
+    }
+    const double scaled =
+        r->scaling == IMEM_ROPE_PLAIN ? theta : theta * (keep + (1.0 - keep) / r->factor);
+    // turns per position are at most 1 / (2 pi), so the product stays below 2^64
+    t.turn[i] = (uint64_t)llrint(ldexp(scaled / tau, 62)) << 2;
+  }
+  t.magnitude = (float)r->magnitude;
+  t.interleaved = r->layout == IMEM_ROPE_INTERLEAVED;
+  t.rot_dim = r->rot_dim;
+  return IMEM_OK;
+}
+
+imem_status imem_rotate(imem_ctx* h, int n_tokens, const int32_t* positions, const void* q,
+                        int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                        int64_t k_stride, void* k_out, int64_t k_out_stride, int inverse,
+                        void* stream) {
+  if (!h) return IMEM_ERR_INVALID_ARG;
+  const Ctx& c = h->c;
+  if (!c.rope.rot_dim || (!q && !k) || (inverse != 0 && inverse != 1)) return IMEM_ERR_INVALID_ARG;
+  IMEM_CHECK(check_tokens(c, 1, n_tokens, nullptr));
+  IMEM_CHECK(check_ptr(positions));
+  if (q) {
+    IMEM_CHECK(check_ptr(q));
+    IMEM_CHECK(check_ptr(q_out));
+    IMEM_CHECK(check_stride(c, &q_stride, c.cfg.n_q_heads));
+    IMEM_CHECK(check_stride(c, &q_out_stride, c.cfg.n_q_heads));
+  }
+  if (k) {
+    IMEM_CHECK(check_ptr(k));
+    IMEM_CHECK(check_ptr(k_out));
+    IMEM_CHECK(check_stride(c, &k_stride, c.cfg.n_kv_heads));
+    IMEM_CHECK(check_stride(c, &k_out_stride, c.cfg.n_kv_heads));
+  }
+  IMEM_CHECK(check_device(c));
+  IMEM_CHECK(wait_pending(h->c, (cudaStream_t)stream));
+  if (!n_tokens) return IMEM_OK;
+  imem::RotateArgs a = {};
+  a.batch = 1;
+  a.n_tokens = n_tokens;
+  a.positions = positions;
+  a.q = q; a.q_stride = q_stride; a.q_out = q_out; a.q_out_stride = q_out_stride;
+  a.k = k; a.k_stride = k_stride; a.k_out = k_out; a.k_out_stride = k_out_stride;
+  a.rotate = 1;
+  a.inverse = inverse;
+  return cuda_status(imem::launch_rotate(c, a, (cudaStream_t)stream));
+}
+
+imem_status imem_append_paged(imem_ctx* h, int batch, int n_tokens, const int32_t* tok_start,
+                              const int32_t* positions, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                              void* q_out, int64_t q_out_stride, int rotate,
+                              const imem_paged* cache, void* stream) {
+  if (!h) return IMEM_ERR_INVALID_ARG;
+  const Ctx& c = h->c;
+  if (rotate != 0 && rotate != 1) return IMEM_ERR_INVALID_ARG;
+  if (rotate && !c.rope.rot_dim) return IMEM_ERR_INVALID_ARG;
+  IMEM_CHECK(check_tokens(c, batch, n_tokens, tok_start));
+  if (positions) IMEM_CHECK(check_ptr(positions));
+  IMEM_CHECK(check_ptr(k));
+  IMEM_CHECK(check_ptr(v));
+  IMEM_CHECK(check_stride(c, &k_stride, c.cfg.n_kv_heads));
+  IMEM_CHECK(check_stride(c, &v_stride, c.cfg.n_kv_heads));
+  if (q) {
+    IMEM_CHECK(check_ptr(q));
+    IMEM_CHECK(check_ptr(q_out));
+    IMEM_CHECK(check_stride(c, &q_stride, c.cfg.n_q_heads));
+    IMEM_CHECK(check_stride(c, &q_out_stride, c.cfg.n_q_heads));
+  }
+  imem::RotateArgs a = {};
+  IMEM_CHECK(check_paged(cache, &a.pg));
+  IMEM_CHECK(check_device(c));
+  IMEM_CHECK(wait_pending(h->c, (cudaStream_t)stream));
+  if (!n_tokens) return IMEM_OK;
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.start = tok_start;
+  a.positions = positions;
+  a.k = k; a.k_stride = k_stride;
+  a.v = v; a.v_stride = v_stride;
+  a.q = q; a.q_stride = q_stride; a.q_out = q_out; a.q_out_stride = q_out_stride;
+  a.rotate = rotate;
+  return cuda_status(imem::launch_rotate(c, a, (cudaStream_t)stream));
+}
+
+imem_status imem_attend_paged(imem_ctx* h, int batch, int n_tokens, const int32_t* tok_start,
+                              int max_new, int max_len, const void* q, int64_t q_stride,
+                              const imem_paged* cache, float scale, void* out, int64_t out_stride,
+                              float* lse, void* stream) {
+  if (!h) return IMEM_ERR_INVALID_ARG;
+  const Ctx& c = h->c;
+  if (!(scale >= 0.f) || isinf(scale)) return IMEM_ERR_INVALID_ARG;
+  IMEM_CHECK(check_tokens(c, batch, n_tokens, tok_start));
+  if (max_new < 0 || max_new > n_tokens || max_len < 0) return IMEM_ERR_SHAPE;
+  IMEM_CHECK(check_ptr(q));
+  IMEM_CHECK(check_ptr(out));
+  if (lse) IMEM_CHECK(check_ptr(lse));
+  IMEM_CHECK(check_stride(c, &q_stride, c.cfg.n_q_heads));
+  IMEM_CHECK(check_stride(c, &out_stride, c.cfg.n_q_heads));
+  imem::AttendArgs a = {};
+  IMEM_CHECK(check_paged(cache, &a.pg));
+  IMEM_CHECK(check_device(c));
+  IMEM_CHECK(wait_pending(h->c, (cudaStream_t)stream));
+  if (!n_tokens || !max_new) return IMEM_OK;
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.max_new = max_new;
+  a.max_len = max_len;
+  a.start = tok_start;
+  a.q = q; a.q_stride = q_stride;
+  a.out = out; a.out_stride = out_stride;
+  a.lse = lse;
+  a.scale = scale == 0.f ? 1.f / sqrtf((float)c.cfg.head_dim) : scale;
+  return cuda_status(imem::launch_attend(c, a, (cudaStream_t)stream));
+}
+
+imem_status imem_gather_paged(imem_ctx* h, int batch, int n, const int32_t* idx, int idx_stride,
+                              const imem_paged* cache, void* K, void* V, int cap, void* stream) {
+  if (!h) return IMEM_ERR_INVALID_ARG;
+  const Ctx& c = h->c;
+  if (batch < 1 || n < 0 || cap < n) return IMEM_ERR_SHAPE;
+  if (idx) {
+    if (idx_stride < n) return IMEM_ERR_SHAPE;
+    IMEM_CHECK(check_ptr(idx));
+  }
+  IMEM_CHECK(check_ptr(K));
+  IMEM_CHECK(check_ptr(V));
+  imem::PagedView pg;
+  IMEM_CHECK(check_paged(cache, &pg));
+  IMEM_CHECK(check_device(c));
+  IMEM_CHECK(wait_pending(h->c, (cudaStream_t)stream));
+  if (!n) return IMEM_OK;
+  return cuda_status(imem::launch_gather_paged(c, batch, n, idx, idx_stride, pg, K, V, cap,
+                                               (cudaStream_t)stream));
+}
+
 imem_status imem_selftest_wait(imem_ctx* h, long long limit_cycles, void* stream) {
   if (!h) return IMEM_ERR_INVALID_ARG;
   if (limit_cycles < 1 || limit_cycles > 2000000000LL) return IMEM_ERR_INVALID_ARG;

@@ -12,6 +12,16 @@
 
 namespace imem {
 
+// The layer's rotation as the kernels take it: per rotated pair the turns per
+// position as a 64-bit fixed-point fraction (position * turn mod 2^64 is the
+// phase), the magnitude and the layout.
+struct RopeTable {
+  uint64_t turn[64];
+  float magnitude;
+  int rot_dim;
+  int interleaved;
+};
+
 // Context of one layer: configuration, weights repacked for the kernels, and
 // a device error word.
 struct Ctx {
@@ -41,6 +51,7 @@ struct Ctx {
   bool pe_pending;           // the last range's work on `side` may still run
   bool pe_compact_pending;   // ... and its selection and compaction too
   int pe_parity;             // candidate buffer of the next range (0 or 1)
+  RopeTable rope;            // rotation of the layer; rot_dim 0: none set
 };
 
 // Indexer rows in the workspace: d_I features padded to 64 bf16 (128 bytes).
@@ -141,6 +152,44 @@ cudaError_t launch_online_score_evict(const Ctx& c, int batch, int B, int cap, c
                                       int32_t* pos_ret, int32_t* next_pos, void* K_ret, void* V_ret,
                                       int32_t* cache_len, float* M, float* bstab, int32_t* evicted,
                                       int* dec_tag, cudaStream_t st);
+
+// ---- rotary positions and the paged cache (rope.cu, paged.cu, attend*.cu) ----
+
+struct PagedView {
+  void* k;
+  void* v;
+  const int32_t* table;    // [batch, max_pages]
+  const int32_t* len;      // [batch], the new tokens included
+  int n_pages, page_log, max_pages;
+};
+
+// imem_rotate (pg.k null: contiguous k_out, no v) and imem_append_paged.
+struct RotateArgs {
+  int batch, n_tokens;
+  const int32_t* start;       // append: [batch + 1] or null
+  const int32_t* positions;   // angles; append: null for the cache positions
+  const void *q, *k, *v;
+  void *q_out, *k_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int rotate, inverse;
+  PagedView pg;
+};
+cudaError_t launch_rotate(const Ctx& c, const RotateArgs& a, cudaStream_t st);
+
+struct AttendArgs {
+  int batch, n_tokens, max_new, max_len;
+  const int32_t* start;       // [batch + 1] or null
+  const void* q;
+  void* out;
+  float* lse;                 // or null
+  int64_t q_stride, out_stride;
+  float scale;
+  PagedView pg;
+};
+cudaError_t launch_attend(const Ctx& c, const AttendArgs& a, cudaStream_t st);
+
+cudaError_t launch_gather_paged(const Ctx& c, int batch, int n, const int32_t* idx, int idx_stride,
+                                const PagedView& pg, void* K, void* V, int cap, cudaStream_t st);
 
 // A kernel whose bounded wait runs out after `limit` cycles (failure-path test).
 cudaError_t launch_wait_selftest(const Ctx& c, long long limit, cudaStream_t st);

@@ -39,6 +39,17 @@ class OnlineState:
     evicted: torch.Tensor         # [b] int32
 
 
+@dataclasses.dataclass
+class PagedCache:
+    """A paged cache of one layer: pages K, V [n_pages, page_size, Hkv, d], the
+    pages of each sequence and its cached length (new tokens included; the
+    caller advances it before a call with new tokens)."""
+    K: torch.Tensor
+    V: torch.Tensor
+    block_table: torch.Tensor     # [b, max_pages] int32
+    kv_len: torch.Tensor          # [b] int32
+
+
 class IndexMemLayer:
     """Context for one layer. ``weights`` holds device tensors W_iq [Hq,d,dI],
     W_ik [H,dI], w_ig [H,Hq] (model dtype), W_phi [r,d], w_gate [Hq,d] (fp32).
@@ -69,6 +80,7 @@ class IndexMemLayer:
                            None if self.moment else weights["w_gate"])
         self._ws = None
         self._ws_key = None
+        self._device = weights["W_ik"].device
 
     @classmethod
     def from_shape(cls, shape, weights, gate_override=None, readout: str = "gated"):
@@ -223,6 +235,184 @@ class IndexMemLayer:
                          on.khat_ret, on.I_ret, on.pos_ret, on.next_pos, st.cache_len,
                          st.K_ret.shape[1], st.M, st.bstab, out, on.evicted, self._ws, stream)
         return out
+
+    # -- rotary positions and the paged cache -----------------------------------
+    def set_rope(self, rot_dim: Optional[int] = None, base: float = 10000.0, layout: str = "half",
+                 scaling: str = "plain", factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                 orig_len: int = 8192, magnitude: float = 1.0):
+        """The layer's rotary positions (rot_dim None: the whole head). scaling:
+        "plain", "linear", "band" (turns low..high over orig_len) or "ramp"
+        (YaRN's, over the pair's index); rot_dim 0 removes the rotation."""
+        if layout not in B_.ROPE_LAYOUTS or scaling not in B_.ROPE_SCALINGS:
+            raise ValueError("layout must be one of %s, scaling one of %s" % (
+                sorted(B_.ROPE_LAYOUTS), sorted(B_.ROPE_SCALINGS)))
+        rot = self.dims["head_dim"] if rot_dim is None else rot_dim
+        B_.set_rope(self.ctx, B_.Rope(rot, B_.ROPE_LAYOUTS[layout], B_.ROPE_SCALINGS[scaling],
+                                      orig_len, base, factor, low, high, magnitude)
+                    if rot else None)
+
+    def new_paged(self, batch: int, n_pages: int, page_size: int, max_pages: int,
+                  device) -> PagedCache:
+        """Empty pages and an empty table (no page assigned: entries -1)."""
+        shape = (n_pages, page_size, self.dims["n_kv_heads"], self.dims["head_dim"])
+        return PagedCache(
+            K=torch.empty(shape, dtype=self.torch_dtype, device=device),
+            V=torch.empty(shape, dtype=self.torch_dtype, device=device),
+            block_table=torch.full((batch, max_pages), -1, dtype=torch.int32, device=device),
+            kv_len=torch.zeros(batch, dtype=torch.int32, device=device))
+
+    def _tokens(self, name: str, x, heads: int, n: Optional[int] = None) -> int:
+        """Checks a token tensor [n, heads, d] (its rows may be strided);
+        returns the row stride."""
+        d = self.dims["head_dim"]
+        sh = x.shape
+        if len(sh) != 3 or sh[1] != heads or sh[2] != d or (n is not None and sh[0] != n):
+            raise ValueError("%s must be [%s, %d, %d], got %s" % (
+                name, "tokens" if n is None else n, heads, d, tuple(sh)))
+        if x.dtype != self.torch_dtype or x.device != self._device:
+            raise ValueError("%s must be %s on %s" % (name, self.torch_dtype, self._device))
+        s = x.stride()
+        if s[2] != 1 or (heads > 1 and s[1] != d):
+            raise ValueError("%s: the heads of a row must be contiguous" % name)
+        return s[0] if sh[0] > 1 else 0
+
+    def _ints(self, name: str, x, shape):
+        if x.dtype != torch.int32 or x.shape != shape or x.device != self._device or \
+                not x.is_contiguous():
+            raise ValueError("%s must be contiguous int32 %s on %s" % (name, tuple(shape),
+                                                                       self._device))
+
+    def _out(self, name: str, out, like, heads: int):
+        """The output tensor (allocated if None) and its row stride."""
+        if out is None:
+            return torch.empty(like.shape, dtype=like.dtype, device=like.device), 0
+        return out, self._tokens(name, out, heads, like.shape[0])
+
+    def _paged(self, c: PagedCache):
+        K, V, bt = c.K, c.V, c.block_table
+        sh = K.shape
+        if len(sh) != 4 or sh[2] != self.dims["n_kv_heads"] or sh[3] != self.dims["head_dim"] or \
+                V.shape != sh or K.dtype != self.torch_dtype or V.dtype != self.torch_dtype or \
+                K.device != self._device or V.device != self._device or \
+                not K.is_contiguous() or not V.is_contiguous():
+            raise ValueError("cache pages must be contiguous %s [n_pages, page_size, %d, %d] on %s"
+                             % (self.torch_dtype, self.dims["n_kv_heads"], self.dims["head_dim"],
+                                self._device))
+        if bt.dim() != 2:
+            raise ValueError("block_table must be [batch, max_pages]")
+        self._ints("block_table", bt, bt.shape)
+        self._ints("kv_len", c.kv_len, bt.shape[:1])
+        return B_.make_paged(K, V, bt, c.kv_len, sh[0], sh[1], bt.shape[1])
+
+    def rotate(self, q, k, positions, q_out=None, k_out=None, inverse: bool = False, stream=None):
+        """Rotary positions: q [T, Hq, d] and k [T, Hkv, d] (either may be None)
+        turned by positions [T]; returns (q_out, k_out). The outputs may be the
+        inputs."""
+        T = (k if q is None else q).shape[0]
+        self._ints("positions", positions, (T,))
+        qs = qos = ks = kos = 0
+        if q is not None:
+            qs = self._tokens("q", q, self.dims["n_q_heads"], T)
+            q_out, qos = self._out("q_out", q_out, q, self.dims["n_q_heads"])
+        if k is not None:
+            ks = self._tokens("k", k, self.dims["n_kv_heads"], T)
+            k_out, kos = self._out("k_out", k_out, k, self.dims["n_kv_heads"])
+        if T:
+            B_.rotate(self.ctx, T, positions, q, qs, q_out if q is not None else None, qos, k, ks,
+                      k_out if k is not None else None, kos, inverse, stream)
+        return q_out, k_out
+
+    def append_paged(self, k, v, cache: PagedCache, tok_start=None, positions=None, q=None,
+                     q_out=None, rotate: bool = True, stream=None):
+        """Writes the new tokens' keys (rotated) and values [T, Hkv, d] into the
+        cache; with q [T, Hq, d] returns the rotated queries. tok_start [b + 1]:
+        the sequences' token ranges (None: equally many each); cache.kv_len
+        already counts the new tokens."""
+        b, T = cache.block_table.shape[0], k.shape[0]
+        pg = self._paged(cache)
+        Hkv = self.dims["n_kv_heads"]
+        ks, vs = self._tokens("k", k, Hkv), self._tokens("v", v, Hkv, T)
+        if tok_start is not None:
+            self._ints("tok_start", tok_start, (b + 1,))
+        if positions is not None:
+            self._ints("positions", positions, (T,))
+        qs = qos = 0
+        if q is not None:
+            qs = self._tokens("q", q, self.dims["n_q_heads"], T)
+            q_out, qos = self._out("q_out", q_out, q, self.dims["n_q_heads"])
+        if T:
+            B_.append_paged(self.ctx, b, T, tok_start, positions, k, ks, v, vs, q, qs,
+                            q_out if q is not None else None, qos, rotate, pg, stream)
+        return q_out if q is not None else None
+
+    def attend_paged(self, q, cache: PagedCache, tok_start=None, max_new: Optional[int] = None,
+                     max_len: Optional[int] = None, scale: Optional[float] = None, out=None,
+                     lse=None, return_lse: bool = False, stream=None):
+        """Causal attention of the new tokens q [T, Hq, d] over the paged cache
+        (their own rows appended before). max_new: most new tokens of a sequence
+        (default: T, or T / b without tok_start); max_len: the longest kv_len
+        expected (a hint; default: what the table can hold). Returns out, or
+        (out, lse [T, Hq] fp32) with return_lse."""
+        b, T = cache.block_table.shape[0], q.shape[0]
+        pg = self._paged(cache)
+        Hq = self.dims["n_q_heads"]
+        qs = self._tokens("q", q, Hq)
+        out, os_ = self._out("out", out, q, Hq)
+        if tok_start is not None:
+            self._ints("tok_start", tok_start, (b + 1,))
+        if lse is not None:
+            if lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous() or \
+                    lse.device != self._device:
+                raise ValueError("lse must be contiguous float32 [%d, %d]" % (T, Hq))
+        elif return_lse:
+            lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+        if max_new is None:
+            max_new = T if tok_start is not None else T // b
+        if max_len is None:
+            max_len = min(pg.max_pages * pg.page_size, 2 ** 31 - 1)
+        if T:
+            B_.attend_paged(self.ctx, b, T, tok_start, max_new, max_len, q, qs, pg,
+                            0.0 if scale is None else scale, out, os_, lse, stream)
+        return (out, lse) if return_lse else out
+
+    def gather_paged(self, cache: PagedCache, idx=None, n: Optional[int] = None, K=None, V=None,
+                     stream=None):
+        """Rows at positions idx [b, n] (None: positions 0..n-1) of the paged
+        cache, to K, V [b, cap >= n, Hkv, d] (allocated if None). Call
+        invalidate_decode after gathering into a cache that decode steps used."""
+        b = cache.block_table.shape[0]
+        pg = self._paged(cache)
+        if idx is None:
+            if n is None:
+                raise ValueError("gather_paged needs idx or n")
+        else:
+            n = idx.shape[-1]
+            self._ints("idx", idx, (b, n))
+        tail = (self.dims["n_kv_heads"], self.dims["head_dim"])
+        if K is None and V is None:
+            K = torch.empty((b, n) + tail, dtype=self.torch_dtype, device=cache.K.device)
+            V = torch.empty((b, n) + tail, dtype=self.torch_dtype, device=cache.K.device)
+        elif K is None or V is None or K.shape != V.shape or K.dim() != 4 or K.shape[0] != b or \
+                K.shape[1] < n or K.shape[2:] != tail or K.dtype != self.torch_dtype or \
+                V.dtype != self.torch_dtype or K.device != self._device or \
+                V.device != self._device or not K.is_contiguous() or not V.is_contiguous():
+            raise ValueError("K and V must be contiguous %s [%d, >= %d, %d, %d] on %s" % (
+                (self.torch_dtype, b, n) + tail + (self._device,)))
+        if n:
+            B_.gather_paged(self.ctx, b, n, idx, n, pg, K, V, K.shape[1], stream)
+        return K, V
+
+    def evict_paged(self, X, Q, cache: PagedCache, st: PrefillState, B: int, chunk: int = 512,
+                    stream=None):
+        """From a paged prompt to the decode state: scores the prompt's hidden
+        states X [b, L, H] and queries Q [b, L, Hq, d], keeps the B most
+        important of its L cached tokens in st's retained cache and adds the
+        others to the memory. Every sequence holds L tokens; the pages are free
+        to be reused once the stream has passed this call."""
+        L = X.shape[1]
+        K, V = self.gather_paged(cache, n=L, stream=stream)
+        self.score_and_evict(X, Q, K, V, st, B, stream=stream)
+        self.update_memory(K, V, st, B, chunk=chunk, stream=stream)
 
     def sync(self, stream=None):
         B_.sync(self.ctx, stream)
