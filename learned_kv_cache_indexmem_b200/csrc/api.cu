@@ -108,6 +108,26 @@ bool make_tmap_bf16(const Ctx& c, CUtensorMap* map, const void* base, uint64_t w
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_tokens(const Ctx& c, CUtensorMap* map, const void* base, uint64_t dim,
+                      uint64_t heads, uint64_t rows, uint64_t stride, uint32_t box_heads,
+                      uint32_t box_rows) {
+  using Fn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                          const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                          CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                          CUtensorMapFloatOOBfill);
+  if (!c.encode_tiled) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64u, box_heads, box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = ((Fn)c.encode_tiled)(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                                          const_cast<void*>(base), dims, strides, box, estr,
+                                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_rows64(const Ctx& c, CUtensorMap* map, const void* base, uint64_t rows,
                       uint32_t box_rows) {
   return make_tmap_bf16(c, map, base, kIdxPad, rows, box_rows);

@@ -1,0 +1,496 @@
+// attend_tc.cu -- causal attention of new tokens over the paged cache, bf16, on
+// the tcgen05 tensor cores.
+//
+//   s_ij = scale q_i . k_j,  o_i = sum_{j <= p_i} softmax(s_i)_j v_j
+//
+// A CTA owns NQ tiles of 128 query rows of one sequence and KV head (row r:
+// new token r / G, head r % G of the group, so K and V are read once for the
+// whole group) and walks the keys in tiles of 128:
+//   producer warp  TMA, page by page, into a ring of 128-row K and V tiles;
+//   MMA warp       S_t = Q_t K^T into TMEM; O_t += P_t V with P_t from TMEM;
+//   4 warps per tile  one row per thread: S from TMEM, running maximum, exp2,
+//                  P as bf16 back into the columns of S, the row's sum.
+// While one tile's softmax runs, the tensor core works on the other tile.
+// MMAs of one thread run in order, so S_t of the next key tile may overwrite
+// P_t once O_t += P_t V has been issued before it, and S_t being complete
+// means that the product before it is: O_t may then be rescaled without a
+// further wait. It is rescaled only when a row's maximum has grown by more than a
+// factor of 2^8 since it was last taken: until then the sums stay below
+// 2^8 times what they would be, far inside fp32 and bf16.
+//
+// Keys past a row's position are masked by selection, so nothing stored there
+// matters; value rows past the last key that any row sees are zeroed in
+// shared memory (0 * NaN would reach O).
+//
+// Bound by the tensor cores and exp2 for long chunks (8192 new tokens at
+// 131072, 32 heads of 128: 29.3 ms, 0.58 PFLOP/s), by HBM for a few tokens.
+//
+// With too few tiles to fill the GPU the keys of a tile are split over a
+// cluster; the states (m, l, O) meet over distributed shared memory and are
+// summed in rank order.
+#include "common.cuh"
+#include "internal.h"
+#include "paged.cuh"
+#include "tc.cuh"
+
+#include <atomic>
+#include <string.h>
+
+namespace imem {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kKeys = 128;       // keys per tile
+constexpr float kGrow = 8.f;     // log2 growth of a maximum that is left alone
+
+template <int D, int NQ> struct TcCfg {
+  static constexpr int threads = NQ * 128 + 128;
+  static constexpr int tile = kKeys * D * 2;                   // bytes of 128 rows
+  static constexpr int half = kKeys * 128;                     // of 64 columns of them
+  static constexpr int stages = D == 128 ? (NQ == 2 ? 5 : 6) : 8;
+  static constexpr int q = 0, ring = NQ * tile;
+  static constexpr int bars = ring + stages * tile;
+  static constexpr int total = bars + 256 + 1024;
+  static constexpr int o_stride = D + 4;                       // floats, merge buffer
+  static constexpr uint32_t tmem_cols = NQ * (128 + D) <= 256 ? 256 : 512;
+  static_assert(NQ * 128 * o_stride * 4 + NQ * 128 * 8 <= bars, "merge buffer fits");
+  static_assert(total <= 232448, "shared memory of a CTA");
+};
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(NQ * 128 + 128, 1)
+attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttendArgs a,
+                 int Hq, int Hkv, int G, int S, int tiles, int* __restrict__ err) {
+  using C = TcCfg<D, NQ>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = tc::smem_addr(smem), sR = sQ + C::ring, bar = sQ + C::bars;
+  const uint32_t q_full = bar, r_full = bar + 8, r_empty = r_full + 8 * C::stages,
+                 s_full = r_empty + 8 * C::stages, p_full = s_full + 8 * NQ, o_full = p_full + 8 * NQ;
+  __shared__ uint32_t s_tmem;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // linear grid, the longest tiles first, heads fastest (neighbours share
+  // nothing but run alike; the tiles of one head meet in L2)
+  int idx = blockIdx.x;
+  const int rank = idx % S;
+  idx /= S;
+  const int h = idx % Hkv;
+  idx /= Hkv;
+  const int seq = idx % a.batch;
+  const int tile = tiles - 1 - idx / a.batch;
+
+  const SeqInfo sq = seq_info(seq, a.batch, a.n_tokens, a.start, a.pg);
+  if (tile == 0 && rank == 0 && h == 0 && tid == 0 && (sq.bad || sq.n > a.max_new))
+    record_error(err, DEV_RANGE);
+  const int n_rows = min(sq.n, a.max_new) * G;
+  const int r0 = tile * (NQ * 128);
+  if (r0 >= n_rows) return;                  // the whole cluster
+  const int past = sq.len - sq.n;            // position of the first new token
+  // keys that the rows of the CTA see, and their tiles of this rank
+  auto keys_of = [&](int row_end) { return max(0, past + (row_end - 1) / G + 1); };
+  const int n_keys = keys_of(min(n_rows, r0 + NQ * 128));
+  const int all = (n_keys + kKeys - 1) / kKeys;
+  const int per = (all + S - 1) / S;
+  const int b0 = min(rank * per, all), n = min(b0 + per, all) - b0;
+  int cnt[NQ];   // of each query tile
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) {
+    const int lo = r0 + t * 128;
+    const int k = lo < n_rows ? keys_of(min(n_rows, lo + 128)) : 0;
+    cnt[t] = min(max((k + kKeys - 1) / kKeys - b0, 0), n);
+  }
+
+  if (tid == 0) {
+    tc::mbar_init(q_full, 1);
+    for (int i = 0; i < C::stages; ++i) {
+      tc::mbar_init(r_full + 8 * i, 1);
+      tc::mbar_init(r_empty + 8 * i, 1);
+    }
+    for (int t = 0; t < NQ; ++t) {
+      tc::mbar_init(s_full + 8 * t, 1);
+      tc::mbar_init(p_full + 8 * t, 4);
+      tc::mbar_init(o_full + 8 * t, 1);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == NQ * 4) {
+    tc::tmem_alloc(tc::smem_addr(&s_tmem), C::tmem_cols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+
+  float m = -INFINITY, l = 0.f;   // softmax threads: this row's state (m: raw scores)
+  const int row = r0 + tid;       // softmax threads: warps 0 .. 4 NQ - 1
+  const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+  const int my = warp >> 2;       // their query tile
+
+  if (n > 0) {
+    if (warp == NQ * 4 + 1) {
+      // ------------------------------------------------------------ producer
+      const int page = 1 << a.pg.page_log;
+      const int box = min(page, kKeys), parts = kKeys / box;   // boxes per tile
+      const int32_t* table = a.pg.table + (long long)seq * a.pg.max_pages;
+      if (lane == 0) {
+        tc::mbar_expect_tx(q_full, NQ * C::tile);
+        for (int t = 0; t < NQ; ++t)
+          for (int c = 0; c < D / 64; ++c)
+            tc::tma_load_3d(sQ + t * C::tile + c * C::half, &mq, q_full, 64 * c, h * G,
+                            sq.tok0 + (r0 + t * 128) / G);
+      }
+      auto page_of = [&](int j) {   // this lane's box of key tile j
+        const int key = (b0 + j) * kKeys + lane * box;
+        return j < n && lane < parts && key < n_keys ? table[key >> a.pg.page_log] : -2;
+      };
+      int next = page_of(0);
+      bool ok = true;
+      for (int j = 0; j < n && ok; ++j) {
+        const int pid = next;
+        next = page_of(j + 1);
+        const bool load = pid >= 0 && pid < a.pg.n_pages;
+        if (pid != -2 && !load) record_error(err, DEV_RANGE);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (D * 2);
+        const int y = (pid << a.pg.page_log) + (((b0 + j) * kKeys) & (page - 1) & ~(box - 1));
+        for (int v = 0; v < 2; ++v) {
+          const int i = 2 * j + v, st = i % C::stages;
+          if (i >= C::stages && !tc::mbar_wait(r_empty + 8 * st, (i / C::stages - 1) & 1)) {
+            record_error(err, DEV_TIMEOUT);
+            ok = false;
+            break;
+          }
+          if (lane == 0) tc::mbar_expect_tx(r_full + 8 * st, bytes);
+          __syncwarp();
+          if (load) {
+            const uint32_t dst = sR + st * C::tile + lane * box * 128;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tc::tma_load_2d(dst + c * C::half, v ? &mv : &mk, r_full + 8 * st, h * D + 64 * c, y);
+          }
+        }
+      }
+    } else if (warp == NQ * 4) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t IQK = tc::idesc(tc::kFmtBF16, 128, kKeys, false, false);
+      constexpr uint32_t IPV = tc::idesc(tc::kFmtBF16, 128, D, false, true);
+      auto wait = [&](uint32_t b, int phase) {
+        const bool ok = tc::mbar_wait(b, phase & 1);
+        if (!ok) record_error(err, DEV_TIMEOUT);
+        return ok;
+      };
+      auto full = [&](int i) { return wait(r_full + 8 * (i % C::stages), i / C::stages); };
+      auto release = [&](int i) {
+        if (lane == 0) tc::mma_commit(r_empty + 8 * (i % C::stages));
+      };
+      auto qk = [&](int t, int j) {   // S_t = Q_t K_j^T
+        if (lane == 0) {
+          const uint32_t q = sQ + t * C::tile, k = sR + ((2 * j) % C::stages) * C::tile;
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (s >> 2) * C::half + (s & 3) * 32;
+            tc::mma_f16(tmem + t * 128, tc::sdesc_sw128(q + off, 16, 1024),
+                        tc::sdesc_sw128(k + off, 16, 1024), IQK, s > 0);
+          }
+          tc::mma_commit(s_full + 8 * t);
+        }
+      };
+      bool ok = wait(q_full, 0) && full(0);
+      if (ok) {
+#pragma unroll
+        for (int t = 0; t < NQ; ++t)
+          if (cnt[t] > 0) qk(t, 0);
+        release(0);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        if (!full(2 * j + 1)) break;
+        const uint32_t v = sR + ((2 * j + 1) % C::stages) * C::tile;
+        const int live = n_keys - (b0 + j) * kKeys;   // rows of this tile that any row sees
+        if (live < kKeys) {
+          for (int i = lane; i < (kKeys - live) * (D / 8); i += 32) {
+            const int r = live + i / (D / 8), c = i % (D / 8);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(
+                             v + (c >> 3) * C::half + r * 128 + (c & 7) * 16), "r"(0u) : "memory");
+          }
+          tc::fence_proxy_async();
+          __syncwarp();
+        }
+        bool have_k = false;
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          if (j >= cnt[t] || !ok) continue;
+          if (!wait(p_full + 8 * t, j)) { ok = false; continue; }
+          tc::fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int s = 0; s < kKeys / 16; ++s)
+              tc::mma_f16_ta(tmem + NQ * 128 + t * D, tmem + t * 128 + s * 8,
+                             tc::sdesc_sw128(v + s * 2048, C::half, 1024), IPV, (j | s) > 0);
+          }
+          if (j + 1 < cnt[t]) {
+            if (!have_k) {
+              if (!full(2 * j + 2)) { ok = false; continue; }
+              have_k = true;
+            }
+            qk(t, j + 1);
+          } else if (lane == 0) {
+            tc::mma_commit(o_full + 8 * t);
+          }
+        }
+        if (!ok) break;
+        release(2 * j + 1);
+        if (have_k) release(2 * j + 2);
+      }
+    } else if (warp < NQ * 4) {
+      // ------------------------------------------------------------ softmax
+      const uint32_t tS = tmem + lane_base + my * 128, tO = tmem + lane_base + NQ * 128 + my * D;
+      const float sl2 = a.scale * kLog2e;
+      const uint64_t scale2 = tc::pack2(sl2, sl2);
+      const int pos = past + row / G;            // rows past n_rows: whatever comes, not written
+      const int warp_pos = past + (row - lane) / G;
+      uint64_t sum = 0;                          // two partial sums
+      bool ok = true;
+      for (int j = 0; j < cnt[my] && ok; ++j) {
+        if (!tc::mbar_wait(s_full + 8 * my, j & 1)) {
+          record_error(err, DEV_TIMEOUT);
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(tS + 32 * c, s[c]);
+        tc::tmem_wait_ld_dep<true>(s[0]);
+#pragma unroll
+        for (int c = 1; c < 4; ++c) tc::tmem_wait_ld_dep<false>(s[c]);
+        const int key0 = (b0 + j) * kKeys;
+        if (key0 + kKeys - 1 > warp_pos) {
+          const int lim = pos - key0;            // columns up to it are seen
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (32 * c + x > lim) s[c][x] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+          for (int x = 2; x < 32; x += 2)
+            mx[c] = tc::max3f(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
+        }
+        const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // NaN when both are -inf: not grown
+        const bool grown = m == -INFINITY ? mj > m : (mj - m) * sl2 > kGrow;
+        float f = 1.f;
+        if (grown) {
+          f = tc::ex2((m - mj) * sl2);
+          m = mj;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, grown)) {
+          float lo, hi;
+          tc::unpack2(sum, lo, hi);
+          sum = tc::pack2(lo * f, hi * f);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tc::tmem_ld32_async(tO + 32 * c, o);
+            tc::tmem_wait_ld_dep<true>(o);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tc::tmem_st32(tO + 32 * c, o);
+          }
+        }
+        const float nm = m == -INFINITY ? 0.f : -m * sl2;
+        const uint64_t nm2 = tc::pack2(nm, nm);
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t p[32];
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            const uint64_t y = tc::fma2(tc::pack2(__uint_as_float(s[c + (x >> 5)][x & 31]),
+                                                  __uint_as_float(s[c + (x >> 5)][(x & 31) + 1])),
+                                        scale2, nm2);
+            float y0, y1;
+            tc::unpack2(y, y0, y1);
+            y0 = tc::ex2(y0);
+            y1 = tc::ex2(y1);
+            sum = tc::add2(sum, tc::pack2(y0, y1));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+            p[x >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          tc::tmem_st32(tS + 16 * c, p);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + 8 * my);
+      }
+      float lo, hi;
+      tc::unpack2(sum, lo, hi);
+      l = lo + hi;
+      if (cnt[my] > 0 && ok && !tc::mbar_wait(o_full + 8 * my, 0)) record_error(err, DEV_TIMEOUT);
+      tc::fence_after();
+    }
+  }
+
+  // ---------------------------------------------------------------- outputs
+  const float sl2 = a.scale * kLog2e;
+  auto out_at = [&](int r) {
+    return (__nv_bfloat16*)a.out + (long long)(sq.tok0 + r / G) * a.out_stride + (h * G + r % G) * D;
+  };
+  auto put_lse = [&](int r, float m2, float ll) {   // m2: maximum of the log2 scores
+    if (a.lse)
+      a.lse[(long long)(sq.tok0 + r / G) * Hq + h * G + r % G] =
+          ll != 0.f ? (m2 + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
+  };
+  const bool mine = warp < NQ * 4 && n > 0 && cnt[my < NQ ? my : 0] > 0;
+  const uint32_t tO = tmem + lane_base + NQ * 128 + my * D;
+  if (S == 1) {
+    if (warp < NQ * 4) {
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (mine) {
+          tc::tmem_ld32_async(tO + 32 * c, o);
+          tc::tmem_wait_ld_dep<true>(o);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0u;
+        }
+        if (row < n_rows) {
+          __nv_bfloat16* p = out_at(row) + 32 * c;
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[x + e]) * inv;
+            store8(p + x, f);
+          }
+        }
+      }
+      if (row < n_rows) put_lse(row, m * sl2, l);
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == NQ * 4) tc::tmem_dealloc(tmem, C::tmem_cols);
+    return;
+  }
+  // states into shared memory (every copy and MMA of the CTA is complete: the
+  // MMA warp waited for the copies, the softmax warps for the last MMA)
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  float* s_o = reinterpret_cast<float*>(smem);
+  float2* s_ml = reinterpret_cast<float2*>(smem + NQ * 128 * C::o_stride * 4);
+  if (warp < NQ * 4) {
+    s_ml[tid] = make_float2(m == -INFINITY ? m : m * sl2, l);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      if (mine) {
+        tc::tmem_ld32_async(tO + 32 * c, o);
+        tc::tmem_wait_ld_dep<true>(o);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = 0u;
+      }
+#pragma unroll
+      for (int x = 0; x < 32; x += 4)
+        *reinterpret_cast<uint4*>(s_o + tid * C::o_stride + 32 * c + x) =
+            make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+    }
+    tc::fence_before();
+  }
+  tc::cluster_sync_all();
+  if (warp == NQ * 4) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, C::tmem_cols);
+  }
+  const uint32_t a_o = tc::smem_addr(s_o), a_ml = tc::smem_addr(s_ml);
+  const int live_rows = min(NQ * 128, n_rows - r0);
+  for (int i = rank * C::threads + tid; i < live_rows * (D / 8); i += S * C::threads) {
+    const int r = i / (D / 8), c = (i % (D / 8)) * 8;
+    float mm = -INFINITY, ll = 0.f, f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    for (int k = 0; k < S; ++k) mm = fmaxf(mm, tc::ld_cluster_v2(tc::mapa(a_ml + 8u * r, k)).x);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    for (int k = 0; k < S; ++k) {
+      const float2 st = tc::ld_cluster_v2(tc::mapa(a_ml + 8u * r, k));
+      const float4 x = tc::ld_cluster_v4(tc::mapa(a_o + 4u * (r * C::o_stride + c), k));
+      const float4 y = tc::ld_cluster_v4(tc::mapa(a_o + 4u * (r * C::o_stride + c + 4), k));
+      const float w = tc::ex2(st.x - base);
+      ll += w * st.y;
+      f[0] += w * x.x; f[1] += w * x.y; f[2] += w * x.z; f[3] += w * x.w;
+      f[4] += w * y.x; f[5] += w * y.y; f[6] += w * y.z; f[7] += w * y.w;
+    }
+    const float inv = ll != 0.f ? 1.f / ll : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= inv;
+    store8(out_at(r0 + r) + c, f);
+    if (c == 0) put_lse(r0 + r, mm, ll);
+  }
+  tc::cluster_sync_all();   // no CTA leaves while its state may still be read
+}
+
+template <int D, int NQ>
+cudaError_t launch(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+  using C = TcCfg<D, NQ>;
+  const int G = c.group, Hkv = c.cfg.n_kv_heads;
+  const int tiles = (a.max_new * G + NQ * 128 - 1) / (NQ * 128);
+  // CTAs that have rows, at least: packed tokens over full tiles
+  const long long busy = ((long long)a.n_tokens * G + NQ * 128 - 1) / (NQ * 128) * Hkv;
+  int S = 1;
+  while (S < 8 && busy * S * 2 <= c.num_sms && (long long)a.max_len >= 4LL * S * kKeys) S *= 2;
+  const long long grid = (long long)tiles * a.batch * Hkv * S;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int box = 1 << (a.pg.page_log < 7 ? a.pg.page_log : 7);
+  CUtensorMap mq, mk, mv;
+  const uint64_t rows = (uint64_t)a.pg.n_pages << a.pg.page_log;
+  if (!make_tmap_tokens(c, &mq, a.q, D, c.cfg.n_q_heads, a.n_tokens, a.q_stride, G, 128 / G) ||
+      !make_tmap_bf16(c, &mk, a.pg.k, (uint64_t)Hkv * D, rows, box) ||
+      !make_tmap_bf16(c, &mv, a.pg.v, (uint64_t)Hkv * D, rows, box))
+    return cudaErrorInvalidValue;
+  auto k = attend_tc_kernel<D, NQ>;
+  static std::atomic<uint64_t> attr_done{0};   // one bit per device
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(attr_done.load() & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::total);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(C::threads, 1, 1);
+  cfg.dynamicSmemBytes = C::total;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, mq, mk, mv, a, c.cfg.n_q_heads, Hkv, G, S, tiles, c.err);
+}
+
+template <int D>
+cudaError_t launch_d(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+  // one query tile where no sequence fills two
+  return a.max_new * c.group <= 128 ? launch<D, 1>(c, a, st) : launch<D, 2>(c, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tc(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+  return c.cfg.head_dim == 128 ? launch_d<128>(c, a, st) : launch_d<64>(c, a, st);
+}
+
+}  // namespace imem

@@ -68,6 +68,12 @@ bool make_tmap_rows64(const Ctx& c, CUtensorMap* map, const void* base, uint64_t
 bool make_tmap_bf16(const Ctx& c, CUtensorMap* map, const void* base, uint64_t width,
                     uint64_t rows, uint32_t box_rows);
 
+// 3-D TMA map over bf16 tokens [rows, heads, dim], the rows `stride` elements
+// apart: box {64, box_heads, box_rows}, 128-byte swizzle, zero fill.
+bool make_tmap_tokens(const Ctx& c, CUtensorMap* map, const void* base, uint64_t dim,
+                      uint64_t heads, uint64_t rows, uint64_t stride, uint32_t box_heads,
+                      uint32_t box_rows);
+
 // Layout of the caller's workspace for (batch, L).
 constexpr int kOnlineMaxCluster = 16;  // KV heads (= CTAs of the online score-and-evict cluster), max
 
@@ -187,6 +193,7 @@ struct AttendArgs {
   PagedView pg;
 };
 cudaError_t launch_attend(const Ctx& c, const AttendArgs& a, cudaStream_t st);
+cudaError_t launch_attend_tc(const Ctx& c, const AttendArgs& a, cudaStream_t st);   // bf16
 
 cudaError_t launch_gather_paged(const Ctx& c, int batch, int n, const int32_t* idx, int idx_stride,
                                 const PagedView& pg, void* K, void* V, int cap, cudaStream_t st);
