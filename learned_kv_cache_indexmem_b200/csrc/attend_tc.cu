@@ -58,6 +58,14 @@ template <int D, int NQ> struct TcCfg {
   static_assert(total <= 232448, "shared memory of a CTA");
 };
 
+// Registers: two query tiles launch with 384 threads x 168; the softmax warps
+// hold a row of S (128 values) and take 216, paid for by the other four warps
+// (256 x 216 + 128 x 72 = 384 x 168; nobody changes its share again, so the
+// softmax warps' request is met as soon as the others have given theirs up).
+// One tile's 256 threads need no split.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= 384 * kRegsLaunch, "register pool");
+
 template <int D, int NQ>
 __global__ void __launch_bounds__(NQ * 128 + 128, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -131,8 +139,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
   const int my = warp >> 2;       // their query tile
 
-  if (n > 0) {
-    if (warp == NQ * 4 + 1) {
+  if (warp >= NQ * 4) {
+    if constexpr (NQ == 2) tc::regs_release<kRegsOther>();
+    if (warp == NQ * 4 + 1 && n > 0) {
       // ------------------------------------------------------------ producer
       const int page = 1 << a.pg.page_log;
       const int box = min(page, kKeys), parts = kKeys / box;   // boxes per tile
@@ -174,7 +183,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
           }
         }
       }
-    } else if (warp == NQ * 4) {
+    } else if (warp == NQ * 4 && n > 0) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t IQK = tc::idesc(tc::kFmtBF16, 128, kKeys, false, false);
       constexpr uint32_t IPV = tc::idesc(tc::kFmtBF16, 128, D, false, true);
@@ -245,102 +254,113 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         release(2 * j + 1);
         if (have_k) release(2 * j + 2);
       }
-    } else if (warp < NQ * 4) {
-      // ------------------------------------------------------------ softmax
-      const uint32_t tS = tmem + lane_base + my * 128, tO = tmem + lane_base + NQ * 128 + my * D;
-      const float sl2 = a.scale * kLog2e;
-      const uint64_t scale2 = tc::pack2(sl2, sl2);
-      const int pos = past + row / G;            // rows past n_rows: whatever comes, not written
-      const int warp_pos = past + (row - lane) / G;
-      uint64_t sum = 0;                          // two partial sums
-      bool ok = true;
-      for (int j = 0; j < cnt[my] && ok; ++j) {
-        if (!tc::mbar_wait(s_full + 8 * my, j & 1)) {
-          record_error(err, DEV_TIMEOUT);
-          ok = false;
-          break;
-        }
-        tc::fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(tS + 32 * c, s[c]);
-        tc::tmem_wait_ld_dep<true>(s[0]);
-#pragma unroll
-        for (int c = 1; c < 4; ++c) tc::tmem_wait_ld_dep<false>(s[c]);
-        const int key0 = (b0 + j) * kKeys;
-        if (key0 + kKeys - 1 > warp_pos) {
-          const int lim = pos - key0;            // columns up to it are seen
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (32 * c + x > lim) s[c][x] = 0xff800000u;
-        }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
-#pragma unroll
-          for (int x = 2; x < 32; x += 2)
-            mx[c] = tc::max3f(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
-        }
-        const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // NaN when both are -inf: not grown
-        const bool grown = m == -INFINITY ? mj > m : (mj - m) * sl2 > kGrow;
-        float f = 1.f;
-        if (grown) {
-          f = tc::ex2((m - mj) * sl2);
-          m = mj;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, grown)) {
-          float lo, hi;
-          tc::unpack2(sum, lo, hi);
-          sum = tc::pack2(lo * f, hi * f);
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tc::tmem_ld32_async(tO + 32 * c, o);
-            tc::tmem_wait_ld_dep<true>(o);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tc::tmem_st32(tO + 32 * c, o);
-          }
-        }
-        const float nm = m == -INFINITY ? 0.f : -m * sl2;
-        const uint64_t nm2 = tc::pack2(nm, nm);
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          uint32_t p[32];
-#pragma unroll
-          for (int x = 0; x < 64; x += 2) {
-            const uint64_t y = tc::fma2(tc::pack2(__uint_as_float(s[c + (x >> 5)][x & 31]),
-                                                  __uint_as_float(s[c + (x >> 5)][(x & 31) + 1])),
-                                        scale2, nm2);
-            float y0, y1;
-            tc::unpack2(y, y0, y1);
-            y0 = tc::ex2(y0);
-            y1 = tc::ex2(y1);
-            sum = tc::add2(sum, tc::pack2(y0, y1));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
-            p[x >> 1] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          tc::tmem_st32(tS + 16 * c, p);
-        }
-        tc::tmem_wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full + 8 * my);
-      }
-      float lo, hi;
-      tc::unpack2(sum, lo, hi);
-      l = lo + hi;
-      if (cnt[my] > 0 && ok && !tc::mbar_wait(o_full + 8 * my, 0)) record_error(err, DEV_TIMEOUT);
-      tc::fence_after();
     }
+    // the CTA's end, in step with the softmax warps'
+    tc::fence_before();
+    __syncthreads();
+    if (S > 1) tc::cluster_sync_all();
+    tc::fence_after();
+    if (warp == NQ * 4) tc::tmem_dealloc(tmem, C::tmem_cols);
+    if (S > 1) tc::cluster_sync_all();
+    return;
+  }
+
+  if constexpr (NQ == 2) tc::regs_take<kRegsSoftmax>();
+  const uint32_t tO = tmem + lane_base + NQ * 128 + my * D;
+  const float sl2 = a.scale * kLog2e;
+  if (n > 0) {
+    // ------------------------------------------------------------ softmax
+    const uint32_t tS = tmem + lane_base + my * 128;
+    const uint64_t scale2 = tc::pack2(sl2, sl2);
+    const int pos = past + row / G;            // rows past n_rows: whatever comes, not written
+    const int warp_pos = past + (row - lane) / G;
+    uint64_t sum = 0;                          // two partial sums
+    bool ok = true;
+    for (int j = 0; j < cnt[my] && ok; ++j) {
+      if (!tc::mbar_wait(s_full + 8 * my, j & 1)) {
+        record_error(err, DEV_TIMEOUT);
+        ok = false;
+        break;
+      }
+      tc::fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(tS + 32 * c, s[c]);
+      tc::tmem_wait_ld_dep<true>(s[0]);
+#pragma unroll
+      for (int c = 1; c < 4; ++c) tc::tmem_wait_ld_dep<false>(s[c]);
+      const int key0 = (b0 + j) * kKeys;
+      if (key0 + kKeys - 1 > warp_pos) {
+        const int lim = pos - key0;            // columns up to it are seen
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (32 * c + x > lim) s[c][x] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+        for (int x = 2; x < 32; x += 2)
+          mx[c] = tc::max3f(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
+      }
+      const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      // NaN when both are -inf: not grown
+      const bool grown = m == -INFINITY ? mj > m : (mj - m) * sl2 > kGrow;
+      float f = 1.f;
+      if (grown) {
+        f = tc::ex2((m - mj) * sl2);
+        m = mj;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, grown)) {
+        float lo, hi;
+        tc::unpack2(sum, lo, hi);
+        sum = tc::pack2(lo * f, hi * f);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tc::tmem_ld32_async(tO + 32 * c, o);
+          tc::tmem_wait_ld_dep<true>(o);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+          tc::tmem_st32(tO + 32 * c, o);
+        }
+      }
+      const float nm = m == -INFINITY ? 0.f : -m * sl2;
+      const uint64_t nm2 = tc::pack2(nm, nm);
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t p[32];
+#pragma unroll
+        for (int x = 0; x < 64; x += 2) {
+          const uint64_t y = tc::fma2(tc::pack2(__uint_as_float(s[c + (x >> 5)][x & 31]),
+                                                __uint_as_float(s[c + (x >> 5)][(x & 31) + 1])),
+                                      scale2, nm2);
+          float y0, y1;
+          tc::unpack2(y, y0, y1);
+          y0 = tc::ex2(y0);
+          y1 = tc::ex2(y1);
+          sum = tc::add2(sum, tc::pack2(y0, y1));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+          p[x >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        tc::tmem_st32(tS + 16 * c, p);
+      }
+      tc::tmem_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(p_full + 8 * my);
+    }
+    float lo, hi;
+    tc::unpack2(sum, lo, hi);
+    l = lo + hi;
+    if (cnt[my] > 0 && ok && !tc::mbar_wait(o_full + 8 * my, 0)) record_error(err, DEV_TIMEOUT);
+    tc::fence_after();
   }
 
   // ---------------------------------------------------------------- outputs
-  const float sl2 = a.scale * kLog2e;
   auto out_at = [&](int r) {
     return (__nv_bfloat16*)a.out + (long long)(sq.tok0 + r / G) * a.out_stride + (h * G + r % G) * D;
   };
@@ -349,48 +369,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
       a.lse[(long long)(sq.tok0 + r / G) * Hq + h * G + r % G] =
           ll != 0.f ? (m2 + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
   };
-  const bool mine = warp < NQ * 4 && n > 0 && cnt[my < NQ ? my : 0] > 0;
-  const uint32_t tO = tmem + lane_base + NQ * 128 + my * D;
+  const bool mine = n > 0 && cnt[my] > 0;
   if (S == 1) {
-    if (warp < NQ * 4) {
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (mine) {
-          tc::tmem_ld32_async(tO + 32 * c, o);
-          tc::tmem_wait_ld_dep<true>(o);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = 0u;
-        }
-        if (row < n_rows) {
-          __nv_bfloat16* p = out_at(row) + 32 * c;
-#pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[x + e]) * inv;
-            store8(p + x, f);
-          }
-        }
-      }
-      if (row < n_rows) put_lse(row, m * sl2, l);
-    }
-    tc::fence_before();
-    __syncthreads();
-    if (warp == NQ * 4) tc::tmem_dealloc(tmem, C::tmem_cols);
-    return;
-  }
-  // states into shared memory (every copy and MMA of the CTA is complete: the
-  // MMA warp waited for the copies, the softmax warps for the last MMA)
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  float* s_o = reinterpret_cast<float*>(smem);
-  float2* s_ml = reinterpret_cast<float2*>(smem + NQ * 128 * C::o_stride * 4);
-  if (warp < NQ * 4) {
-    s_ml[tid] = make_float2(m == -INFINITY ? m : m * sl2, l);
+    const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -401,21 +382,50 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] = 0u;
       }
+      if (row < n_rows) {
+        __nv_bfloat16* p = out_at(row) + 32 * c;
 #pragma unroll
-      for (int x = 0; x < 32; x += 4)
-        *reinterpret_cast<uint4*>(s_o + tid * C::o_stride + 32 * c + x) =
-            make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+        for (int x = 0; x < 32; x += 8) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[x + e]) * inv;
+          store8(p + x, f);
+        }
+      }
     }
+    if (row < n_rows) put_lse(row, m * sl2, l);
     tc::fence_before();
+    __syncthreads();
+    return;
   }
+  // states into shared memory (every copy and MMA of the CTA is complete: the
+  // MMA warp waited for the copies, the softmax warps for the last MMA)
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  float* s_o = reinterpret_cast<float*>(smem);
+  float2* s_ml = reinterpret_cast<float2*>(smem + NQ * 128 * C::o_stride * 4);
+  s_ml[tid] = make_float2(m == -INFINITY ? m : m * sl2, l);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    if (mine) {
+      tc::tmem_ld32_async(tO + 32 * c, o);
+      tc::tmem_wait_ld_dep<true>(o);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[x] = 0u;
+    }
+#pragma unroll
+    for (int x = 0; x < 32; x += 4)
+      *reinterpret_cast<uint4*>(s_o + tid * C::o_stride + 32 * c + x) =
+          make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+  }
+  tc::fence_before();
   tc::cluster_sync_all();
-  if (warp == NQ * 4) {
-    tc::fence_after();
-    tc::tmem_dealloc(tmem, C::tmem_cols);
-  }
   const uint32_t a_o = tc::smem_addr(s_o), a_ml = tc::smem_addr(s_ml);
   const int live_rows = min(NQ * 128, n_rows - r0);
-  for (int i = rank * C::threads + tid; i < live_rows * (D / 8); i += S * C::threads) {
+  for (int i = rank * (NQ * 128) + tid; i < live_rows * (D / 8); i += S * (NQ * 128)) {
     const int r = i / (D / 8), c = (i % (D / 8)) * 8;
     float mm = -INFINITY, ll = 0.f, f[8];
 #pragma unroll

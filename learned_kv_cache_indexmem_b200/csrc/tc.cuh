@@ -318,6 +318,15 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
+// Registers per thread of the executing warpgroup (all four warps): the
+// released ones return to the block's pool, taken ones wait for it.
+template <int N> __device__ __forceinline__ void regs_release() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 // Two fp32 operations in one instruction (sm_100).
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
