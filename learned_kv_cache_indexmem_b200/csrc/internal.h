@@ -193,7 +193,10 @@ struct AttendArgs {
   PagedView pg;
 };
 cudaError_t launch_attend(const Ctx& c, const AttendArgs& a, cudaStream_t st);
-cudaError_t launch_attend_tc(const Ctx& c, const AttendArgs& a, cudaStream_t st);   // bf16
+// bf16: long chunks; at most 24 query rows per sequence and KV head
+cudaError_t launch_attend_tc(const Ctx& c, const AttendArgs& a, cudaStream_t st);
+bool attend_step_fits(const Ctx& c, const AttendArgs& a);
+cudaError_t launch_attend_step(const Ctx& c, const AttendArgs& a, cudaStream_t st);
 
 cudaError_t launch_gather_paged(const Ctx& c, int batch, int n, const int32_t* idx, int idx_stride,
                                 const PagedView& pg, void* K, void* V, int cap, cudaStream_t st);

@@ -81,6 +81,8 @@ class IndexMemLayer:
         self._ws = None
         self._ws_key = None
         self._device = weights["W_ik"].device
+        self._index = weights["W_ik"].get_device()
+        self._hq, self._hkv, self._d = n_q_heads, n_kv_heads, head_dim
 
     @classmethod
     def from_shape(cls, shape, weights, gate_override=None, readout: str = "gated"):
@@ -261,48 +263,46 @@ class IndexMemLayer:
             block_table=torch.full((batch, max_pages), -1, dtype=torch.int32, device=device),
             kv_len=torch.zeros(batch, dtype=torch.int32, device=device))
 
-    def _tokens(self, name: str, x, heads: int, n: Optional[int] = None) -> int:
+    # The checks below run on every call of a decode step: few attribute reads,
+    # the explanation only where one fails.
+    def _tokens(self, name: str, x, n: int, heads: int) -> int:
         """Checks a token tensor [n, heads, d] (its rows may be strided);
         returns the row stride."""
-        d = self.dims["head_dim"]
-        sh = x.shape
-        if len(sh) != 3 or sh[1] != heads or sh[2] != d or (n is not None and sh[0] != n):
-            raise ValueError("%s must be [%s, %d, %d], got %s" % (
-                name, "tokens" if n is None else n, heads, d, tuple(sh)))
-        if x.dtype != self.torch_dtype or x.device != self._device:
-            raise ValueError("%s must be %s on %s" % (name, self.torch_dtype, self._device))
-        s = x.stride()
-        if s[2] != 1 or (heads > 1 and s[1] != d):
-            raise ValueError("%s: the heads of a row must be contiguous" % name)
-        return s[0] if sh[0] > 1 else 0
+        d, s = self._d, x.stride()
+        if x.shape == (n, heads, d) and x.dtype is self.torch_dtype and \
+                x.get_device() == self._index and s[2] == 1 and (s[1] == d or heads == 1):
+            return s[0] if n > 1 else 0
+        raise ValueError("%s must be %s [%d, %d, %d] on %s, the heads of a row contiguous; got %s %s"
+                         " with strides %s on %s" % (name, self.torch_dtype, n, heads, d,
+                                                     self._device, x.dtype, tuple(x.shape), s,
+                                                     x.device))
 
     def _ints(self, name: str, x, shape):
-        if x.dtype != torch.int32 or x.shape != shape or x.device != self._device or \
+        if x.dtype is not torch.int32 or x.shape != shape or x.get_device() != self._index or \
                 not x.is_contiguous():
             raise ValueError("%s must be contiguous int32 %s on %s" % (name, tuple(shape),
                                                                        self._device))
 
-    def _out(self, name: str, out, like, heads: int):
+    def _out(self, name: str, out, like, n: int, heads: int):
         """The output tensor (allocated if None) and its row stride."""
         if out is None:
-            return torch.empty(like.shape, dtype=like.dtype, device=like.device), 0
-        return out, self._tokens(name, out, heads, like.shape[0])
+            return torch.empty_like(like, memory_format=torch.contiguous_format), 0
+        return out, self._tokens(name, out, n, heads)
 
     def _paged(self, c: PagedCache):
-        K, V, bt = c.K, c.V, c.block_table
-        sh = K.shape
-        if len(sh) != 4 or sh[2] != self.dims["n_kv_heads"] or sh[3] != self.dims["head_dim"] or \
-                V.shape != sh or K.dtype != self.torch_dtype or V.dtype != self.torch_dtype or \
-                K.device != self._device or V.device != self._device or \
-                not K.is_contiguous() or not V.is_contiguous():
+        K, V, table = c.K, c.V, c.block_table
+        sh, ts, dt, dev = K.shape, table.shape, self.torch_dtype, self._index
+        if len(sh) != 4 or sh[2] != self._hkv or sh[3] != self._d or V.shape != sh or \
+                K.dtype is not dt or V.dtype is not dt or K.get_device() != dev or \
+                V.get_device() != dev or not K.is_contiguous() or not V.is_contiguous():
             raise ValueError("cache pages must be contiguous %s [n_pages, page_size, %d, %d] on %s"
-                             % (self.torch_dtype, self.dims["n_kv_heads"], self.dims["head_dim"],
-                                self._device))
-        if bt.dim() != 2:
+                             % (dt, self._hkv, self._d, self._device))
+        if len(ts) != 2:
             raise ValueError("block_table must be [batch, max_pages]")
-        self._ints("block_table", bt, bt.shape)
-        self._ints("kv_len", c.kv_len, bt.shape[:1])
-        return B_.make_paged(K, V, bt, c.kv_len, sh[0], sh[1], bt.shape[1])
+        self._ints("block_table", table, ts)
+        self._ints("kv_len", c.kv_len, ts[:1])
+        return B_.Paged(K.data_ptr(), V.data_ptr(), table.data_ptr(), c.kv_len.data_ptr(), sh[0],
+                        sh[1], ts[1]), ts[0]
 
     def rotate(self, q, k, positions, q_out=None, k_out=None, inverse: bool = False, stream=None):
         """Rotary positions: q [T, Hq, d] and k [T, Hkv, d] (either may be None)
@@ -311,15 +311,18 @@ class IndexMemLayer:
         T = (k if q is None else q).shape[0]
         self._ints("positions", positions, (T,))
         qs = qos = ks = kos = 0
-        if q is not None:
-            qs = self._tokens("q", q, self.dims["n_q_heads"], T)
-            q_out, qos = self._out("q_out", q_out, q, self.dims["n_q_heads"])
-        if k is not None:
-            ks = self._tokens("k", k, self.dims["n_kv_heads"], T)
-            k_out, kos = self._out("k_out", k_out, k, self.dims["n_kv_heads"])
+        if q is None:
+            q_out = None
+        else:
+            qs = self._tokens("q", q, T, self._hq)
+            q_out, qos = self._out("q_out", q_out, q, T, self._hq)
+        if k is None:
+            k_out = None
+        else:
+            ks = self._tokens("k", k, T, self._hkv)
+            k_out, kos = self._out("k_out", k_out, k, T, self._hkv)
         if T:
-            B_.rotate(self.ctx, T, positions, q, qs, q_out if q is not None else None, qos, k, ks,
-                      k_out if k is not None else None, kos, inverse, stream)
+            B_.rotate(self.ctx, T, positions, q, qs, q_out, qos, k, ks, k_out, kos, inverse, stream)
         return q_out, k_out
 
     def append_paged(self, k, v, cache: PagedCache, tok_start=None, positions=None, q=None,
@@ -328,22 +331,23 @@ class IndexMemLayer:
         cache; with q [T, Hq, d] returns the rotated queries. tok_start [b + 1]:
         the sequences' token ranges (None: equally many each); cache.kv_len
         already counts the new tokens."""
-        b, T = cache.block_table.shape[0], k.shape[0]
-        pg = self._paged(cache)
-        Hkv = self.dims["n_kv_heads"]
-        ks, vs = self._tokens("k", k, Hkv), self._tokens("v", v, Hkv, T)
+        pg, b = self._paged(cache)
+        T = k.shape[0]
+        ks, vs = self._tokens("k", k, T, self._hkv), self._tokens("v", v, T, self._hkv)
         if tok_start is not None:
             self._ints("tok_start", tok_start, (b + 1,))
         if positions is not None:
             self._ints("positions", positions, (T,))
         qs = qos = 0
-        if q is not None:
-            qs = self._tokens("q", q, self.dims["n_q_heads"], T)
-            q_out, qos = self._out("q_out", q_out, q, self.dims["n_q_heads"])
+        if q is None:
+            q_out = None
+        else:
+            qs = self._tokens("q", q, T, self._hq)
+            q_out, qos = self._out("q_out", q_out, q, T, self._hq)
         if T:
-            B_.append_paged(self.ctx, b, T, tok_start, positions, k, ks, v, vs, q, qs,
-                            q_out if q is not None else None, qos, rotate, pg, stream)
-        return q_out if q is not None else None
+            B_.append_paged(self.ctx, b, T, tok_start, positions, k, ks, v, vs, q, qs, q_out, qos,
+                            rotate, pg, stream)
+        return q_out
 
     def attend_paged(self, q, cache: PagedCache, tok_start=None, max_new: Optional[int] = None,
                      max_len: Optional[int] = None, scale: Optional[float] = None, out=None,
@@ -353,16 +357,15 @@ class IndexMemLayer:
         (default: T, or T / b without tok_start); max_len: the longest kv_len
         expected (a hint; default: what the table can hold). Returns out, or
         (out, lse [T, Hq] fp32) with return_lse."""
-        b, T = cache.block_table.shape[0], q.shape[0]
-        pg = self._paged(cache)
-        Hq = self.dims["n_q_heads"]
-        qs = self._tokens("q", q, Hq)
-        out, os_ = self._out("out", out, q, Hq)
+        pg, b = self._paged(cache)
+        T, Hq = q.shape[0], self._hq
+        qs = self._tokens("q", q, T, Hq)
+        out, os_ = self._out("out", out, q, T, Hq)
         if tok_start is not None:
             self._ints("tok_start", tok_start, (b + 1,))
         if lse is not None:
-            if lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous() or \
-                    lse.device != self._device:
+            if lse.dtype is not torch.float32 or lse.shape != (T, Hq) or \
+                    not lse.is_contiguous() or lse.get_device() != self._index:
                 raise ValueError("lse must be contiguous float32 [%d, %d]" % (T, Hq))
         elif return_lse:
             lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
@@ -380,18 +383,16 @@ class IndexMemLayer:
         """Rows at positions idx [b, n] (None: positions 0..n-1) of the paged
         cache, to K, V [b, cap >= n, Hkv, d] (allocated if None). Call
         invalidate_decode after gathering into a cache that decode steps used."""
-        b = cache.block_table.shape[0]
-        pg = self._paged(cache)
+        pg, b = self._paged(cache)
         if idx is None:
             if n is None:
                 raise ValueError("gather_paged needs idx or n")
         else:
             n = idx.shape[-1]
             self._ints("idx", idx, (b, n))
-        tail = (self.dims["n_kv_heads"], self.dims["head_dim"])
+        tail = (self._hkv, self._d)
         if K is None and V is None:
-            K = torch.empty((b, n) + tail, dtype=self.torch_dtype, device=cache.K.device)
-            V = torch.empty((b, n) + tail, dtype=self.torch_dtype, device=cache.K.device)
+            K, V = cache.K.new_empty((b, n) + tail), cache.K.new_empty((b, n) + tail)
         elif K is None or V is None or K.shape != V.shape or K.dim() != 4 or K.shape[0] != b or \
                 K.shape[1] < n or K.shape[2:] != tail or K.dtype != self.torch_dtype or \
                 V.dtype != self.torch_dtype or K.device != self._device or \
