@@ -21,6 +21,7 @@
 #include "tc.cuh"
 
 #include <atomic>
+#include <mutex>
 
 namespace imem {
 namespace {
@@ -39,7 +40,11 @@ template <int D, int NT> struct StepCfg {
   static constexpr int bars = stages * 2 * tile;
   static constexpr int o_stride = D + 4;
   static constexpr int part = NT * 8 * o_stride * 4 + NT * 8 * 8;   // one warp's state
-  static constexpr int total = bars + 128 + 1024;
+  // three column tiles leave no registers for q: its fragments are read from
+  // shared memory (rows 16 bytes apart in banks) for every 16 keys
+  static constexpr bool q_smem = NT == 3;
+  static constexpr int q_row = D * 2 + 16, q = bars + 128;
+  static constexpr int total = q + (q_smem ? NT * 8 * q_row : 0) + 1024;
   static_assert(kWarps * part <= bars, "the states take the ring's place");
 };
 
@@ -148,9 +153,23 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     // -------------------------------------------------------------- consumers
     const float sl2 = a.scale * kLog2e;
     // q as B fragments: row 8 nt + g, dims 16 s + 2 t and + 8
-    uint32_t q0[NT][D / 16], q1[NT][D / 16];
+    constexpr int QR = C::q_smem ? 1 : NT;
+    uint32_t q0[QR][D / 16], q1[QR][D / 16];
+    if constexpr (C::q_smem) {
+      for (int i = tid; i < NT * 8 * (D / 8); i += kWarps * 32) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (r < n_rows)
+          x = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+                                              (long long)(sq.tok0 + r / G) * a.q_stride +
+                                              (h * G + r % G) * D + c * 8);
+        *reinterpret_cast<uint4*>(smem + C::q + r * C::q_row + c * 16) = x;
+      }
+      asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps * 32) : "memory");
+    }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < QR; ++nt) {
+      if constexpr (C::q_smem) break;
       const int r = 8 * nt + g;
       const bool on = r < n_rows;
       const uint32_t* p = (const uint32_t*)((const __nv_bfloat16*)a.q +
@@ -195,12 +214,25 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       for (int nt = 0; nt < NT; ++nt)
         s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = s2[nt][0] = s2[nt][1] = s2[nt][2] = s2[nt][3] = 0.f;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const int c = 2 * k + (lane >> 4);
-        uint32_t af[4];
-        ldsm4(kt + (c >> 3) * C::half + kr * 128 + (((c & 7) ^ (kr & 7)) << 4), af);
+      for (int k = 0; k < D / 16; k += 2) {   // two chains of products per score
+        uint32_t af[2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16(k & 1 ? s2[nt] : s[nt], af, q0[nt][k], q1[nt][k]);
+        for (int u = 0; u < 2; ++u) {
+          const int c = 2 * (k + u) + (lane >> 4);
+          ldsm4(kt + (c >> 3) * C::half + kr * 128 + (((c & 7) ^ (kr & 7)) << 4), af[u]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (C::q_smem) {
+            uint32_t b[4];   // chunks 2 k .. 2 k + 3 of rows 8 nt ..
+            ldsm4(sR + C::q + (8 * nt + (lane & 7)) * C::q_row + (2 * k + (lane >> 3)) * 16, b);
+            mma16(s[nt], af[0], b[0], b[1]);
+            mma16(s2[nt], af[1], b[2], b[3]);
+          } else {
+            mma16(s[nt], af[0], q0[nt][k], q1[nt][k]);
+            mma16(s2[nt], af[1], q0[nt][k + 1], q1[nt][k + 1]);
+          }
+        }
       }
       uint32_t p0[NT], p1[NT];
       float f[NT][2];
@@ -322,31 +354,65 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   if (S > 1) tc::cluster_sync_all();   // no CTA leaves while its state may still be read
 }
 
-// CTAs per sequence and KV head. Two CTAs fit an SM. If the units do not fill
-// one wave, split until they do, two stages per CTA at least; else split into
-// several waves, so that ragged lengths even out, 1024 keys per CTA at least.
-int step_splits(const Ctx& c, const AttendArgs& a) {
+// CTAs per sequence and KV head (a cluster). Where the units fit one wave, as
+// many as keep it one wave (clusters must fit the GPU's processor groups, so
+// the driver is asked how many of each size are resident: 32 clusters of 9 do
+// not all fit 148 SMs at two CTAs each, and a second wave doubled the time of
+// four sequences of 16384 keys), two stages per CTA at least. Else several
+// waves, so that ragged lengths even out, 1024 keys per CTA at least.
+int step_splits(const Ctx& c, const AttendArgs& a, const int (&resident)[17]) {
   const int seqs = a.batch < a.n_tokens ? a.batch : a.n_tokens;   // sequences with new tokens, at most
   const long long units = (long long)seqs * c.cfg.n_kv_heads;
-  const int slots = 2 * c.num_sms;
-  long long S, most;
-  if (units * 2 <= slots) {
-    S = slots / units;
-    most = (a.max_len + 2 * kRows - 1) / (2 * kRows);
-  } else {
-    S = (4 * slots + units - 1) / units;
-    most = a.max_len / 1024;
+  if (units <= resident[2]) {
+    const int most = (a.max_len + 2 * kRows - 1) / (2 * kRows);
+    for (int S = most < 16 ? most : 16; S > 1; --S)
+      if (resident[S] >= units) return S;
+    return 1;
   }
-  if (S > most) S = most;
-  if (S > 16) S = 16;
-  return S < 1 ? 1 : (int)S;
+  long long S = (4LL * resident[1] + units - 1) / units;
+  if (S > a.max_len / 1024) S = a.max_len / 1024;
+  return S < 1 ? 1 : S > 16 ? 16 : (int)S;
 }
 
 template <int D, int NT>
 cudaError_t launch(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
   using C = StepCfg<D, NT>;
   const int Hkv = c.cfg.n_kv_heads;
-  const int S = step_splits(c, a);
+  auto k = attend_step_kernel<D, NT>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::total;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // once per device: attributes, and how many clusters of each size are resident
+  static std::atomic<const int (*)[17]> setup[64];
+  static std::mutex setup_mu;
+  const int dv = c.device & 63;
+  const int(*resident)[17] = setup[dv].load(std::memory_order_acquire);
+  if (!resident) {
+    std::lock_guard<std::mutex> lock(setup_mu);
+    resident = setup[dv].load(std::memory_order_relaxed);
+    if (!resident) {
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::total);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      static int table[64][17];
+      for (int s = 1; s <= 16 && e == cudaSuccess; ++s) {
+        cfg.gridDim = dim3(s, 1, 1);
+        attr[0].val.clusterDim.x = s;
+        e = cudaOccupancyMaxActiveClusters(&table[dv][s], k, &cfg);
+      }
+      if (e != cudaSuccess) return e;
+      resident = &table[dv];
+      setup[dv].store(resident, std::memory_order_release);
+    }
+  }
+  const int S = step_splits(c, a, *resident);
   const long long grid = (long long)a.batch * Hkv * S;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int box = 1 << (a.pg.page_log < 6 ? a.pg.page_log : 6);
@@ -355,27 +421,9 @@ cudaError_t launch(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
   if (!make_tmap_bf16(c, &mk, a.pg.k, (uint64_t)Hkv * D, rows, box) ||
       !make_tmap_bf16(c, &mv, a.pg.v, (uint64_t)Hkv * D, rows, box))
     return cudaErrorInvalidValue;
-  auto k = attend_step_kernel<D, NT>;
-  static std::atomic<uint64_t> attr_done{0};   // one bit per device
-  const uint64_t bit = 1ull << (c.device & 63);
-  if (!(attr_done.load() & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::total);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    attr_done.fetch_or(bit);
-  }
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = C::total;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k, mk, mv, a, c.cfg.n_q_heads, Hkv, c.group, S, c.err);
 }
 
