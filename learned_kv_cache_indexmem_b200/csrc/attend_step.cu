@@ -45,7 +45,7 @@ template <int D, int NT> struct StepCfg {
   static constexpr bool q_smem = NT == 3;
   static constexpr int q_row = D * 2 + 16, q = bars + 128;
   static constexpr int total = q + (q_smem ? NT * 8 * q_row : 0) + 1024;
-  static_assert(kWarps * part <= bars, "the states take the ring's place");
+  static_assert((kWarps + 1) * part <= bars, "the states take the ring's place");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -297,11 +297,10 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
 
   // the warps' states take the ring's place (every stage has been consumed)
   __syncthreads();
-  const int state = C::part / 4;   // floats of a warp's state: O rows, then (m, l)
-  float* s_st = reinterpret_cast<float*>(smem);
+  float* s_st = reinterpret_cast<float*>(smem);   // per warp: O rows, then (m, l)
   const float sl2 = a.scale * kLog2e;
   if (warp < kWarps) {
-    float* so = s_st + warp * state;
+    float* so = s_st + warp * (C::part / 4);
     float2* ml = reinterpret_cast<float2*>(so + NT * 8 * C::o_stride);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -317,30 +316,9 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       }
     }
   }
-  if (S > 1) tc::cluster_sync_all();
-  else __syncthreads();
-  const uint32_t base_o = sR, base_ml = sR + NT * 8 * C::o_stride * 4;
-  for (int i = rank * kThreads + tid; i < n_rows * (D / 4); i += S * kThreads) {
-    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float mm = -INFINITY, ll = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
-    for (int k = 0; k < S; ++k) {
-      const uint32_t at = tc::mapa(base_ml + 8u * r, k);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, tc::ld_cluster_v2(at + w * C::part).x);
-    }
-    const float base = mm == -INFINITY ? 0.f : mm;
-    for (int k = 0; k < S; ++k) {
-      const uint32_t at = tc::mapa(base_ml + 8u * r, k);
-      const uint32_t ao = tc::mapa(base_o + 4u * (r * C::o_stride + c), k);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 sm = tc::ld_cluster_v2(at + w * C::part);
-        const float4 y = tc::ld_cluster_v4(ao + w * C::part);
-        const float f = tc::ex2(sm.x - base);
-        ll += f * sm.y;
-        x0 += f * y.x; x1 += f * y.y; x2 += f * y.z; x3 += f * y.w;
-      }
-    }
+  __syncthreads();
+
+  auto finish = [&](int r, int c, float mm, float ll, float x0, float x1, float x2, float x3) {
     const float inv = ll != 0.f ? 1.f / ll : 0.f;
     const long long tok = sq.tok0 + r / G;
     const int head = h * G + r % G;
@@ -350,8 +328,66 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
         make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
     if (c == 0 && a.lse)
       a.lse[tok * Hq + head] = ll != 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
+  };
+  // the CTA's state: its warps' meet here
+  const int items = n_rows * (D / 4);
+  float* c_o = s_st + kWarps * (C::part / 4);
+  float2* c_ml = reinterpret_cast<float2*>(c_o + NT * 8 * C::o_stride);
+  for (int i = tid; i < items; i += kThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float2 ml[kWarps];
+    float4 y[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float* so = s_st + w * (C::part / 4);
+      ml[w] = reinterpret_cast<const float2*>(so + NT * 8 * C::o_stride)[r];
+      y[w] = *reinterpret_cast<const float4*>(so + r * C::o_stride + c);
+    }
+    const float mm = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = tc::ex2(ml[w].x - base);
+      ll += f * ml[w].y;
+      x.x += f * y[w].x; x.y += f * y[w].y; x.z += f * y[w].z; x.w += f * y[w].w;
+    }
+    if (S == 1) {
+      finish(r, c, mm, ll, x.x, x.y, x.z, x.w);
+    } else {
+      *reinterpret_cast<float4*>(c_o + r * C::o_stride + c) = x;
+      if (c == 0) c_ml[r] = make_float2(mm, ll);
+    }
   }
-  if (S > 1) tc::cluster_sync_all();   // no CTA leaves while its state may still be read
+  if (S == 1) return;
+  tc::cluster_sync_all();
+  // the cluster's: 16 lanes per item, one for each CTA's state, so that all the
+  // remote reads of an item are in flight at once
+  const uint32_t a_o = tc::smem_addr(c_o), a_ml = tc::smem_addr(c_ml);
+  constexpr int kGroups = kThreads / 16;
+  const int k = lane & 15;
+  for (int i0 = rank * kGroups; i0 < items; i0 += S * kGroups) {
+    const int i = i0 + (tid >> 4);
+    const int r = min(i, items - 1) / (D / 4), c = (min(i, items - 1) % (D / 4)) * 4;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < S) {
+      ml = tc::ld_cluster_v2(tc::mapa(a_ml + 8u * r, k));
+      x = tc::ld_cluster_v4(tc::mapa(a_o + 4u * (r * C::o_stride + c), k));
+    }
+    float mm = ml.x;
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+    const float f = tc::ex2(ml.x - (mm == -INFINITY ? 0.f : mm));
+    float v[5] = {f * ml.y, f * x.x, f * x.y, f * x.z, f * x.w};
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+#pragma unroll
+      for (int e = 0; e < 5; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], d);
+    if (k == 0 && i < items) finish(r, c, mm, v[0], v[1], v[2], v[3], v[4]);
+  }
+  tc::cluster_sync_all();   // no CTA leaves while its state may still be read
 }
 
 // CTAs per sequence and KV head (a cluster). Where the units fit one wave, as
