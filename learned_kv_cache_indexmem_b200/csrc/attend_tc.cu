@@ -11,7 +11,9 @@
 //   4 warps per tile  one row per thread: S from TMEM, running maximum, exp2,
 //                  P as bf16 back into the columns of S, the row's sum.
 // While one tile's softmax runs, the tensor core works on the other tile.
-// MMAs of one thread run in order, so S_t of the next key tile may overwrite
+// The MMA warp's loop stays converged and one elected lane issues: its operands
+// are then uniform (a branch on the lane cost 11 %: 474 against 426 us for 2048
+// tokens at 16384 keys; a warp per query tile 562 us). MMAs of one thread run in order, so S_t of the next key tile may overwrite
 // P_t once O_t += P_t V has been issued before it, and S_t being complete
 // means that the product before it is: O_t may then be rescaled without a
 // further wait. It is rescaled only when a row's maximum has grown by more than a
@@ -23,7 +25,7 @@
 // shared memory (0 * NaN would reach O).
 //
 // Bound by the tensor cores and exp2 for long chunks (8192 new tokens at
-// 131072, 32 heads of 128: 15.3 ms, 1.12 PFLOP/s), by HBM for a few tokens.
+// 131072, 32 heads of 128: 14.1 ms, 1.21 PFLOP/s), by HBM for a few tokens.
 //
 // With too few tiles to fill the GPU the keys of a tile are split over a
 // cluster; the states (m, l, O) meet over distributed shared memory and are
@@ -34,7 +36,7 @@
 #include "tc.cuh"
 
 #include <atomic>
-#include <string.h>
+#include <type_traits>
 
 namespace imem {
 namespace {
@@ -44,12 +46,41 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKeys = 128;       // keys per tile
 constexpr float kGrow = 8.f;     // log2 growth of a maximum that is left alone
 
+// 2^y for two values y >= -126 (below: 2^-126) on the FMA units: y = n + f with
+// n the nearest integer (added and taken off 1.5 * 2^23), 2^f on [-1/2, 1/2]
+// by the polynomial of degree 5 with the smallest largest relative error
+// (fitted by the exchange algorithm; 2.4e-7 in fp32, ex2.approx has 1.2e-7), n
+// added to the exponent. The special-function unit gives 16 results per clock
+// and SM, the tensor cores wait for 16384 per tile: sharing them out between
+// the two units shortens the softmax.
+__device__ __forceinline__ void exp2_fma(uint64_t y, float& e0, float& e1) {
+  const uint64_t magic = tc::pack2(12582912.f, 12582912.f);
+  const uint64_t nmagic = tc::pack2(-12582912.f, -12582912.f);
+  float y0, y1;
+  tc::unpack2(y, y0, y1);
+  y = tc::pack2(fmaxf(y0, -126.f), fmaxf(y1, -126.f));
+  const uint64_t t = tc::add2(y, magic);
+  const uint64_t f = tc::fma2(tc::add2(t, nmagic), tc::pack2(-1.f, -1.f), y);
+  auto c2 = [](float c) { return tc::pack2(c, c); };
+  uint64_t p = tc::fma2(f, c2(0.0013276472454890609f), c2(0.009675540961325169f));
+  p = tc::fma2(f, p, c2(0.05550713092088699f));
+  p = tc::fma2(f, p, c2(0.24022120237350464f));
+  p = tc::fma2(f, p, c2(0.6931469440460205f));
+  p = tc::fma2(f, p, c2(1.0000001192092896f));
+  float p0, p1, t0, t1;
+  tc::unpack2(p, p0, p1);
+  tc::unpack2(t, t0, t1);
+  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+constexpr int kFmaOf8 = 1;       // of 8 neighbouring pairs, those taken by exp2_fma (0: 2 % slower, 3: 2 %)
+
 template <int D, int NQ> struct TcCfg {
   static constexpr int threads = NQ * 128 + 128;
   static constexpr int tile = kKeys * D * 2;                   // bytes of 128 rows
   static constexpr int half = kKeys * 128;                     // of 64 columns of them
   static constexpr int stages = D == 128 ? (NQ == 2 ? 5 : 6) : 8;
-  static constexpr int q = 0, ring = NQ * tile;
+  static constexpr int ring = NQ * tile;                       // behind Q
   static constexpr int bars = ring + stages * tile;
   static constexpr int total = bars + 256 + 1024;
   static constexpr int o_stride = D + 4;                       // floats, merge buffer
@@ -77,7 +108,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = tc::smem_addr(smem), sR = sQ + C::ring, bar = sQ + C::bars;
   const uint32_t q_full = bar, r_full = bar + 8, r_empty = r_full + 8 * C::stages,
-                 s_full = r_empty + 8 * C::stages, p_full = s_full + 8 * NQ, o_full = p_full + 8 * NQ;
+                 s_full = r_empty + 8 * C::stages, p_full = s_full + 8 * NQ, o_full = p_full + 16 * NQ;
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -120,7 +151,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     }
     for (int t = 0; t < NQ; ++t) {
       tc::mbar_init(s_full + 8 * t, 1);
-      tc::mbar_init(p_full + 8 * t, 4);
+      tc::mbar_init(p_full + 16 * t, 4);
+      tc::mbar_init(p_full + 16 * t + 8, 4);
       tc::mbar_init(o_full + 8 * t, 1);
     }
     tc::fence_mbar_init();
@@ -194,16 +226,20 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
       };
       auto full = [&](int i) { return wait(r_full + 8 * (i % C::stages), i / C::stages); };
       auto release = [&](int i) {
-        if (lane == 0) tc::mma_commit(r_empty + 8 * (i % C::stages));
+        if (tc::elect_one()) tc::mma_commit(r_empty + 8 * (i % C::stages));
       };
       auto qk = [&](int t, int j) {   // S_t = Q_t K_j^T
-        if (lane == 0) {
-          const uint32_t q = sQ + t * C::tile, k = sR + ((2 * j) % C::stages) * C::tile;
+        if (tc::elect_one()) {
+          // descriptors step by 32 bytes along K within a 64-column half
+          uint64_t dq = tc::sdesc_sw128(sQ + t * C::tile, 16, 1024);
+          uint64_t dk = tc::sdesc_sw128(sR + ((2 * j) % C::stages) * C::tile, 16, 1024);
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = (s >> 2) * C::half + (s & 3) * 32;
-            tc::mma_f16(tmem + t * 128, tc::sdesc_sw128(q + off, 16, 1024),
-                        tc::sdesc_sw128(k + off, 16, 1024), IQK, s > 0);
+          for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              tc::mma_f16(tmem + t * 128, dq + 2 * s, dk + 2 * s, IQK, (c | s) > 0);
+            dq += C::half >> 4;
+            dk += C::half >> 4;
           }
           tc::mma_commit(s_full + 8 * t);
         }
@@ -228,25 +264,27 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
           tc::fence_proxy_async();
           __syncwarp();
         }
-        bool have_k = false;
+        const bool have_k = j + 1 < n;
+        if (have_k && !full(2 * j + 2)) break;
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
           if (j >= cnt[t] || !ok) continue;
-          if (!wait(p_full + 8 * t, j)) { ok = false; continue; }
-          tc::fence_after();
-          if (lane == 0) {
 #pragma unroll
-            for (int s = 0; s < kKeys / 16; ++s)
-              tc::mma_f16_ta(tmem + NQ * 128 + t * D, tmem + t * 128 + s * 8,
-                             tc::sdesc_sw128(v + s * 2048, C::half, 1024), IPV, (j | s) > 0);
-          }
-          if (j + 1 < cnt[t]) {
-            if (!have_k) {
-              if (!full(2 * j + 2)) { ok = false; continue; }
-              have_k = true;
+          for (int hf = 0; hf < 2; ++hf) {   // 64 keys each
+            const uint64_t dv = tc::sdesc_sw128(v + hf * 8192, C::half, 1024);
+            if (!ok || !wait(p_full + 16 * t + 8 * hf, j)) { ok = false; continue; }
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s)   // 16 keys: 2 KB of V, 8 columns of P
+                tc::mma_f16_ta(tmem + NQ * 128 + t * D, tmem + t * 128 + 32 * hf + s * 8,
+                               dv + 128 * s, IPV, (j | hf | s) > 0);
             }
+          }
+          if (!ok) continue;
+          if (j + 1 < cnt[t]) {
             qk(t, j + 1);
-          } else if (lane == 0) {
+          } else if (tc::elect_one()) {
             tc::mma_commit(o_full + 8 * t);
           }
         }
@@ -290,7 +328,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll
       for (int c = 1; c < 4; ++c) tc::tmem_wait_ld_dep<false>(s[c]);
       const int key0 = (b0 + j) * kKeys;
-      if (key0 + kKeys - 1 > warp_pos) {
+      const bool edge = key0 + kKeys - 1 > warp_pos;
+      if (edge) {
         const int lim = pos - key0;            // columns up to it are seen
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -330,28 +369,40 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
       }
       const float nm = m == -INFINITY ? 0.f : -m * sl2;
       const uint64_t nm2 = tc::pack2(nm, nm);
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {
+      // two halves of 64 keys, each handed to the tensor core as it is done
+      auto half = [&](int hf, auto masked) {
         uint32_t p[32];
 #pragma unroll
         for (int x = 0; x < 64; x += 2) {
-          const uint64_t y = tc::fma2(tc::pack2(__uint_as_float(s[c + (x >> 5)][x & 31]),
-                                                __uint_as_float(s[c + (x >> 5)][(x & 31) + 1])),
-                                      scale2, nm2);
-          float y0, y1;
-          tc::unpack2(y, y0, y1);
-          y0 = tc::ex2(y0);
-          y1 = tc::ex2(y1);
-          sum = tc::add2(sum, tc::pack2(y0, y1));
-          const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+          const uint32_t(&v)[32] = s[2 * hf + (x >> 5)];
+          const uint64_t y = tc::fma2(
+              tc::pack2(__uint_as_float(v[x & 31]), __uint_as_float(v[(x & 31) + 1])), scale2, nm2);
+          float e0, e1;
+          // masked scores are -inf: exactly 0 from the special-function unit
+          if (!decltype(masked)::value && ((x >> 1) * kFmaOf8) % 8 < kFmaOf8) {
+            exp2_fma(y, e0, e1);
+          } else {
+            tc::unpack2(y, e0, e1);
+            e0 = tc::ex2(e0);
+            e1 = tc::ex2(e1);
+          }
+          sum = tc::add2(sum, tc::pack2(e0, e1));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
           p[x >> 1] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        tc::tmem_st32(tS + 16 * c, p);
+        tc::tmem_st32(tS + 32 * hf, p);
+        tc::tmem_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + 8 * (2 * my + hf));
+      };
+      if (edge) {
+        half(0, std::true_type());
+        half(1, std::true_type());
+      } else {
+        half(0, std::false_type());
+        half(1, std::false_type());
       }
-      tc::tmem_wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(p_full + 8 * my);
     }
     float lo, hi;
     tc::unpack2(sum, lo, hi);
