@@ -1,282 +1,385 @@
-// attend.cu -- causal attention of new tokens over the paged cache in fp32
-// arithmetic: every case of the fp32 model dtype.
+// attend.cu -- causal attention of new tokens over the paged cache: the choice
+// of the kernel, and the kernel of the fp32 model dtype.
 //
 //   s_ij = scale q_i . k_j,  o_i = sum_{j <= p_i} softmax(s_i)_j v_j
 //
-// One pass over the keys with the running maximum and sum of the softmax
-// (m, l, O rescaled when m grows). A tile's rows are the new tokens of one
-// sequence times the G query heads of one KV head (row r: token r / G, head
-// r % G), so that K and V are read once for the whole group. The keys of a
-// tile are split over a cluster of CTAs when there are too few tiles to fill
-// the GPU; their states (m, l, O) meet over distributed shared memory, summed
-// in rank order.
+// fp32 products on the tensor cores. A value is split into hi (its upper 11
+// significant bits, the operand format tf32) and lo = x - hi (exact; its upper
+// 11 bits are kept), and a product becomes hi hi + hi lo + lo hi with fp32
+// accumulation: what is dropped is below 3 * 2^-22 of |x y|, next to the 2^-24
+// per addition that any fp32 sum of d products rounds by. Bound by the
+// warp-level MMA: one m16n8k8 (tf32) or m16n8k16 (bf16) per 16 clocks and SM
+// quarter, so three tf32 products cost half of what six bf16 ones of a
+// three-way split do per value, and both beat the fp32 units as far as shared
+// memory feeds those (1024 new tokens, 8 heads of 64: 56 us on them, 47-51
+// us with three bf16 parts, 40 us here; 46 TFLOP/s at 8192 keys).
+//
+// A tile's rows are the new tokens of one sequence times the G query heads of
+// one KV head (row r: token r / G, head r % G), so that K and V are read once
+// for the whole group. Stages of keys come by cp.async, one ahead. Each of four
+// warps has 16 rows (KS = 1), or, with at most 16 rows in all, the same rows
+// and a quarter of each stage's keys (KS = 4). The contraction's index order
+// is free: queries and keys are taken four dimensions a lane (one 16-byte load
+// for an MMA step), values four columns a lane.
+//
+// The keys of a tile are split over a cluster of CTAs when there are too few
+// tiles to fill the GPU; the states (m, l, O) meet over distributed shared
+// memory, summed in a fixed order.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"
 #include "tc.cuh"
 
 #include <atomic>
-#include <type_traits>
 
 namespace imem {
 namespace {
 
-constexpr int kSimtThreads = 256;
-constexpr int kSimtKeys = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 128;
+constexpr float kGrow = 8.f;             // log2 growth of a maximum that is left alone
 
-template <int D, int BM> struct SimtSmem {
-  static constexpr int QS = D + 4, PS = kSimtKeys + 4;
-  static constexpr size_t q = 0;
-  static constexpr size_t k = q + sizeof(float) * BM * QS;
-  static constexpr size_t v = k + sizeof(float) * kSimtKeys * QS;
-  static constexpr size_t p = v + sizeof(float) * kSimtKeys * QS;
-  static constexpr size_t total = p + sizeof(float) * BM * PS;
+template <int D, int KS> struct F32Cfg {
+  static constexpr int keys = KS == 1 ? 32 : 64;             // per stage
+  // row strides in floats: 16-byte loads of neighbouring rows (K: rows g, V:
+  // rows 2 t) then fall on different banks
+  static constexpr int ks = D + 16, vs = D + 4, os = D + 4;
+  static constexpr int k = keys * ks, v = keys * vs;       // floats of a buffer
+  static constexpr int total = 2 * (k + v) * 4;
+  static constexpr int state = 16 * os + 32;                 // a warp's (m, l, O), floats
+  static_assert((KS == 1 ? 4 : 5) * state * 4 <= total, "the states take the buffers' place");
 };
 
-// BM rows (16 * RM) per tile; thread (ty, tx) of 16 x 16 owns rows ty * RM ..
-// and keys tx + 16 j of the scores, dims 4 tx + 64 c of the output.
-template <typename T, int D, int BM>
-__global__ void __launch_bounds__(kSimtThreads)
-attend_simt_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, int tiles,
-                   int* __restrict__ err) {
-  constexpr int RM = BM / 16, DC = D / 64;
-  constexpr int QS = SimtSmem<D, BM>::QS, PS = SimtSmem<D, BM>::PS;
-  extern __shared__ float smem[];
-  float* s_q = smem;
-  float* s_k = smem + SimtSmem<D, BM>::k / 4;
-  float* s_v = smem + SimtSmem<D, BM>::v / 4;
-  float* s_p = smem + SimtSmem<D, BM>::p / 4;
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(tc::smem_addr(dst)),
+               "l"(src), "r"(valid ? 16 : 0) : "memory");   // 0: zero-filled
+}
+// x = hi + lo, hi with 11 significant bits
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// C (16 x 8) += A (16 x 8) B (8 x 8), tf32 operands
+__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int rank = blockIdx.x % S;
-  const int tile = tiles - 1 - blockIdx.x / S;   // the longest first
-  const int h = blockIdx.y, seq = blockIdx.z;
+template <int D, int KS>
+__global__ void __launch_bounds__(kThreads)
+attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, int tiles,
+                  int* __restrict__ err) {
+  using C = F32Cfg<D, KS>;
+  constexpr int kKeys = C::keys;
+  constexpr int NT = kKeys / 8 / KS;       // 8-key tiles of a warp per stage
+  constexpr int BM = 64 / KS;              // rows of the CTA
+  extern __shared__ __align__(16) float smem[];
+  float* s_k = smem;
+  float* s_v = smem + 2 * C::k;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int Hkv = Hq / G;
+  int idx = blockIdx.x;
+  const int rank = idx % S;
+  idx /= S;
+  const int h = idx % Hkv;
+  idx /= Hkv;
+  const int seq = idx % a.batch;
+  const int tile = tiles - 1 - idx / a.batch;   // the longest first
   const SeqInfo sq = seq_info(seq, a.batch, a.n_tokens, a.start, a.pg);
   if (tile == 0 && rank == 0 && h == 0 && tid == 0 && (sq.bad || sq.n > a.max_new))
     record_error(err, DEV_RANGE);
   const int n_rows = min(sq.n, a.max_new) * G;
   const int r0 = tile * BM;
-  if (r0 >= n_rows) return;   // the whole cluster
+  if (r0 >= n_rows) return;         // the whole cluster
   const int past = sq.len - sq.n;   // position of the first new token
   const int n_tile = min(BM, n_rows - r0);
-  // keys the tile sees: up to its last row's position
   const int n_keys = max(0, past + (r0 + n_tile - 1) / G + 1);
-  const int blocks = (n_keys + kSimtKeys - 1) / kSimtKeys;
+  const int blocks = (n_keys + kKeys - 1) / kKeys;
   const int per = (blocks + S - 1) / S;
   const int b0 = min(rank * per, blocks), b1 = min(b0 + per, blocks);
-
-  // queries, as they are (the scale goes on the scores)
-  for (int i = tid; i < BM * (D / 4); i += kSimtThreads) {
-    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < n_tile) {
-      const int rr = r0 + r;
-      const T* p = (const T*)a.q + (long long)(sq.tok0 + rr / G) * a.q_stride + (h * G + rr % G) * D + c;
-      if constexpr (std::is_same<T, float>::value) {
-        x = *reinterpret_cast<const float4*>(p);
-      } else {
-        x = make_float4(Elem<T>::to_f(p[0]), Elem<T>::to_f(p[1]), Elem<T>::to_f(p[2]), Elem<T>::to_f(p[3]));
-      }
-    }
-    *reinterpret_cast<float4*>(s_q + r * QS + c) = x;
-  }
-
-  float o[RM][DC][4], m[RM], l[RM];
-#pragma unroll
-  for (int i = 0; i < RM; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < DC; ++c) o[i][c][0] = o[i][c][1] = o[i][c][2] = o[i][c][3] = 0.f;
-  }
-  const float sl2 = a.scale * kLog2e;
   const int32_t* table = a.pg.table + (long long)seq * a.pg.max_pages;
-  const int Hkv = Hq / G;
+
+  // a stage's keys and values; rows that no row of the tile sees become zeros
+  auto issue = [&](int b, int buf) {
+    constexpr int CH = D / 4, STEP = kThreads / CH, N = kKeys / STEP;
+    const int c = (tid % CH) * 4, first = b * kKeys + tid / CH;
+    // all table entries first: their latencies overlap
+    int page[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int key = first + i * STEP;
+      page[i] = key < n_keys ? __ldg(table + (key >> a.pg.page_log)) : -1;
+    }
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int key = first + i * STEP, r = tid / CH + i * STEP;
+      const bool in = page[i] >= 0 && page[i] < a.pg.n_pages;
+      bad |= key < n_keys && !in;
+      const long long row = ((long long)(in ? page[i] : 0) << a.pg.page_log) +
+                            (key & ((1 << a.pg.page_log) - 1));
+      const long long at = (row * Hkv + h) * D + c;
+      copy16(s_k + buf * C::k + r * C::ks + c, (const float*)a.pg.k + at, in);
+      copy16(s_v + buf * C::v + r * C::vs + c, (const float*)a.pg.v + at, in);
+    }
+    if (bad) record_error(err, DEV_RANGE);
+    asm volatile("cp.async.commit_group;\n" ::);
+  };
+  if (b0 < b1) issue(b0, 0);
+
+  // this lane's rows g and g + 8 of the warp's 16, and their queries: step 2 u
+  // of the contraction takes dimensions 16 u + 4 t and + 1, step 2 u + 1 the next two
+  const int w_row = (KS == 1 ? warp * 16 : 0) + g;
+  float q[2][D / 4];
+  int pos[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = r0 + w_row + 8 * e, rr = min(r, n_rows - 1);
+    pos[e] = past + rr / G;
+    const float* p = (const float*)a.q + (long long)(sq.tok0 + rr / G) * a.q_stride + (h * G + rr % G) * D;
+#pragma unroll
+    for (int u = 0; u < D / 16; ++u) {
+      const float4 x = *reinterpret_cast<const float4*>(p + 16 * u + 4 * t);
+      q[e][4 * u] = x.x; q[e][4 * u + 1] = x.y; q[e][4 * u + 2] = x.z; q[e][4 * u + 3] = x.w;
+    }
+  }
+  // O: tile i holds, for column 2 t + e, dimension 4 (2 t + e) + 32 (i / 4) + i % 4
+  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  const float sl2 = a.scale * kLog2e;
 
   for (int b = b0; b < b1; ++b) {
-    const int key0 = b * kSimtKeys;
-    __syncthreads();
-    for (int i = tid; i < kSimtKeys * (D / 4); i += kSimtThreads) {
-      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (key0 + r < n_keys) {
-        const long long row = cache_row(a.pg, table, key0 + r);
-        if (row >= 0) {
-          const T* kp = (const T*)a.pg.k + (row * Hkv + h) * D + c;
-          const T* vp = (const T*)a.pg.v + (row * Hkv + h) * D + c;
-          if constexpr (std::is_same<T, float>::value) {
-            x = *reinterpret_cast<const float4*>(kp);
-            y = *reinterpret_cast<const float4*>(vp);
-          } else {
-            x = make_float4(Elem<T>::to_f(kp[0]), Elem<T>::to_f(kp[1]), Elem<T>::to_f(kp[2]), Elem<T>::to_f(kp[3]));
-            y = make_float4(Elem<T>::to_f(vp[0]), Elem<T>::to_f(vp[1]), Elem<T>::to_f(vp[2]), Elem<T>::to_f(vp[3]));
-          }
-        } else if (c == 0) {
-          record_error(err, DEV_RANGE);
-        }
-      }
-      *reinterpret_cast<float4*>(s_k + r * QS + c) = x;
-      *reinterpret_cast<float4*>(s_v + r * QS + c) = y;
-    }
-    __syncthreads();
-    float s[RM][4];
-#pragma unroll
-    for (int i = 0; i < RM; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < D; c += 4) {
-      float4 q[RM], k[4];
-#pragma unroll
-      for (int i = 0; i < RM; ++i) q[i] = *reinterpret_cast<const float4*>(s_q + (ty * RM + i) * QS + c);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(s_k + (tx + 16 * j) * QS + c);
-#pragma unroll
-      for (int i = 0; i < RM; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          s[i][j] += q[i].x * k[j].x + q[i].y * k[j].y + q[i].z * k[j].z + q[i].w * k[j].w;
-    }
-#pragma unroll
-    for (int i = 0; i < RM; ++i) {
-      const int rr = r0 + ty * RM + i;
-      const int pos = rr < n_rows ? past + rr / G : -1;
-      float mx = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = key0 + tx + 16 * j <= pos ? s[i][j] * sl2 : -INFINITY;
-        mx = fmaxf(mx, s[i][j]);
-      }
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      const float mn = fmaxf(m[i], mx);
-      const float base = mn == -INFINITY ? 0.f : mn;   // a row with no key yet
-      const float f = exp2f(m[i] - base);
-      m[i] = mn;
-      l[i] *= f;
-#pragma unroll
-      for (int c = 0; c < DC; ++c) { o[i][c][0] *= f; o[i][c][1] *= f; o[i][c][2] *= f; o[i][c][3] *= f; }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = exp2f(s[i][j] - base);
-        l[i] += p;
-        s_p[(ty * RM + i) * PS + tx + 16 * j] = p;
-      }
-    }
-    __syncwarp();   // a row's scores stay within one half warp
-#pragma unroll 2
-    for (int kk = 0; kk < kSimtKeys; kk += 4) {
-      float4 p[RM];
-#pragma unroll
-      for (int i = 0; i < RM; ++i) p[i] = *reinterpret_cast<const float4*>(s_p + (ty * RM + i) * PS + kk);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-#pragma unroll
-        for (int c = 0; c < DC; ++c) {
-          const float4 v = *reinterpret_cast<const float4*>(s_v + (kk + u) * QS + 4 * tx + 64 * c);
-#pragma unroll
-          for (int i = 0; i < RM; ++i) {
-            const float pu = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
-            o[i][c][0] += pu * v.x; o[i][c][1] += pu * v.y; o[i][c][2] += pu * v.z; o[i][c][3] += pu * v.w;
-          }
-        }
-      }
-    }
-  }
-
-#pragma unroll
-  for (int i = 0; i < RM; ++i)
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-
-  auto write = [&](int r, int c, float x0, float x1, float x2, float x3) {
-    const int rr = r0 + r;
-    T* p = (T*)a.out + (long long)(sq.tok0 + rr / G) * a.out_stride + (h * G + rr % G) * D + c;
-    if constexpr (std::is_same<T, float>::value) {
-      *reinterpret_cast<float4*>(p) = make_float4(x0, x1, x2, x3);
+    const int buf = (b - b0) & 1;
+    if (b + 1 < b1) {
+      issue(b + 1, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;\n" ::: "memory");
     } else {
-      p[0] = Elem<T>::from_f(x0); p[1] = Elem<T>::from_f(x1);
-      p[2] = Elem<T>::from_f(x2); p[3] = Elem<T>::from_f(x3);
+      asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     }
-  };
-  auto write_lse = [&](int r, float mm, float ll) {
-    const int rr = r0 + r;
-    if (a.lse)
-      a.lse[(long long)(sq.tok0 + rr / G) * Hq + h * G + rr % G] =
-          ll != 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
-  };
+    __syncthreads();
+    const int w_key = KS == 1 ? 0 : (warp % KS) * 8 * NT;   // the warp's keys of the stage
+    const float* kb = s_k + buf * C::k + (w_key + g) * C::ks + 4 * t;
+    const float* vb = s_v + buf * C::v + (w_key + 2 * t) * C::vs + 4 * g;
+    float s[NT][4], lo[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      lo[i][0] = lo[i][1] = lo[i][2] = lo[i][3] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < D / 16; ++u) {
+      uint32_t ah[2][4], al[2][4], bh[NT][4], bl[NT][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          split(q[e][4 * u + 2 * k], ah[k][e], al[k][e]);
+          split(q[e][4 * u + 2 * k + 1], ah[k][2 + e], al[k][2 + e]);
+        }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(kb + i * 8 * C::ks + 16 * u);
+        split(x.x, bh[i][0], bl[i][0]);
+        split(x.y, bh[i][1], bl[i][1]);
+        split(x.z, bh[i][2], bl[i][2]);
+        split(x.w, bh[i][3], bl[i][3]);
+      }
+      // one product of every tile before the next: a dependent MMA waits for
+      // its accumulator several times as long as the unit takes for it
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) mma8(lo[i], al[k], bh[i][2 * k], bh[i][2 * k + 1]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) mma8(s[i], ah[k], bh[i][2 * k], bh[i][2 * k + 1]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) mma8(lo[i], ah[k], bl[i][2 * k], bl[i][2 * k + 1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] += lo[i][e];
+    // columns 2 t, 2 t + 1 of tile i: keys 8 i + 2 t (+ 1); rows g (0, 1), g + 8 (2, 3)
+    const int key0 = b * kKeys + w_key + 2 * t;
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (key0 + 8 * i + (e & 1) > pos[e >> 1]) s[i][e] = -INFINITY;
+        mx[e >> 1] = fmaxf(mx[e >> 1], s[i][e]);
+      }
+    float f[2];
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+      const bool grown = m[e] == -INFINITY ? mx[e] > m[e] : (mx[e] - m[e]) * sl2 > kGrow;
+      f[e] = grown ? tc::ex2((m[e] - mx[e]) * sl2) : 1.f;
+      if (grown) m[e] = mx[e];
+      any |= grown;
+      const float nm = m[e] == -INFINITY ? 0.f : -m[e] * sl2;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        s[i][2 * e] = tc::ex2(fmaf(s[i][2 * e], sl2, nm));
+        s[i][2 * e + 1] = tc::ex2(fmaf(s[i][2 * e + 1], sl2, nm));
+        sum += s[i][2 * e] + s[i][2 * e + 1];
+      }
+      l[e] = l[e] * f[e] + sum;
+    }
+    if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= f[0]; o[i][1] *= f[0]; o[i][2] *= f[1]; o[i][3] *= f[1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      // step i: index t is key 8 i + 2 t, index t + 4 the key after it
+      uint32_t ah[4], al[4];
+      split(s[i][0], ah[0], al[0]);
+      split(s[i][2], ah[1], al[1]);
+      split(s[i][1], ah[2], al[2]);
+      split(s[i][3], ah[3], al[3]);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const float4 x = *reinterpret_cast<const float4*>(vb + 8 * i * C::vs + 32 * c);
+        const float4 y = *reinterpret_cast<const float4*>(vb + (8 * i + 1) * C::vs + 32 * c);
+        const float v[2][4] = {{x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}};
+        uint32_t vh[2][4], vl[2][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          split(v[0][k], vh[0][k], vl[0][k]);
+          split(v[1][k], vh[1][k], vl[1][k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma8(o[4 * c + k], al, vh[0][k], vh[1][k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma8(o[4 * c + k], ah, vl[0][k], vl[1][k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma8(o[4 * c + k], ah, vh[0][k], vh[1][k]);
+      }
+    }
+    __syncthreads();   // the buffer may be filled again
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+  }
 
-  if (S == 1) {
+  // states: one of 16 rows for each warp, in the buffers' place
 #pragma unroll
-    for (int i = 0; i < RM; ++i) {
-      const int r = ty * RM + i;
-      if (r >= n_tile) continue;
-      const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
-#pragma unroll
-      for (int c = 0; c < DC; ++c)
-        write(r, 4 * tx + 64 * c, o[i][c][0] * inv, o[i][c][1] * inv, o[i][c][2] * inv, o[i][c][3] * inv);
-      if (tx == 0) write_lse(r, m[i], l[i]);
+  for (int e = 0; e < 2; ++e) {
+    float* so = smem + warp * C::state;
+    const int r = g + 8 * e;
+    if (t == 0) {
+      so[16 * C::os + 2 * r] = m[e] == -INFINITY ? m[e] : m[e] * sl2;
+      so[16 * C::os + 2 * r + 1] = l[e];
     }
-    return;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < D / 8; i += 4)
+        *reinterpret_cast<float4*>(so + r * C::os + 4 * (2 * t + c) + 8 * i) =
+            make_float4(o[i][2 * e + c], o[i + 1][2 * e + c], o[i + 2][2 * e + c], o[i + 3][2 * e + c]);
   }
-  // states into this CTA's shared memory (over Q and K), then every CTA of the
-  // cluster merges its share of the output
   __syncthreads();
-  float2* s_ml = reinterpret_cast<float2*>(s_p);
-  float* s_o = s_q;   // [BM][D]
-#pragma unroll
-  for (int i = 0; i < RM; ++i) {
-    const int r = ty * RM + i;
-    if (tx == 0) s_ml[r] = make_float2(m[i], l[i]);
-#pragma unroll
-    for (int c = 0; c < DC; ++c)
-      *reinterpret_cast<float4*>(s_o + r * D + 4 * tx + 64 * c) = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
-  }
-  tc::cluster_sync_all();
-  const uint32_t a_ml = tc::smem_addr(s_ml), a_o = tc::smem_addr(s_o);
-  for (int i = rank * kSimtThreads + tid; i < n_tile * (D / 4); i += S * kSimtThreads) {
-    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float mm = -INFINITY, ll = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < S; ++k) {
-      const float2 st = tc::ld_cluster_v2(tc::mapa(a_ml + 8u * r, k));
-      mm = fmaxf(mm, st.x);
-    }
-    const float base = mm == -INFINITY ? 0.f : mm;
-    for (int k = 0; k < S; ++k) {
-      const float2 st = tc::ld_cluster_v2(tc::mapa(a_ml + 8u * r, k));
-      const float4 y = tc::ld_cluster_v4(tc::mapa(a_o + 4u * (r * D + c), k));
-      const float w = exp2f(st.x - base);
-      ll += w * st.y;
-      x.x += w * y.x; x.y += w * y.y; x.z += w * y.z; x.w += w * y.w;
-    }
+  auto finish = [&](int r, int c, float mm, float ll, float4 x) {
+    const int rr = r0 + r;
+    const long long tok = sq.tok0 + rr / G;
+    const int head = h * G + rr % G;
     const float inv = ll != 0.f ? 1.f / ll : 0.f;
-    write(r, c, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    if (c == 0) write_lse(r, mm, ll);
+    *reinterpret_cast<float4*>((float*)a.out + tok * a.out_stride + head * D + c) =
+        make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (c == 0 && a.lse)
+      a.lse[tok * Hq + head] = ll != 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
+  };
+  // sums N states of one row, `at` giving (m, l) and four columns of the k-th
+  auto meet = [&](int N, auto at, float& mm, float& ll, float4& x) {
+    mm = -INFINITY;
+    ll = 0.f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < N; ++k) {
+      float2 ml;
+      float4 y;
+      at(k, ml, y);
+      const float top = fmaxf(mm, ml.x), base = top == -INFINITY ? 0.f : top;
+      const float fa = tc::ex2(mm - base), fb = tc::ex2(ml.x - base);
+      mm = top;
+      ll = ll * fa + ml.y * fb;
+      x.x = x.x * fa + y.x * fb; x.y = x.y * fa + y.y * fb;
+      x.z = x.z * fa + y.z * fb; x.w = x.w * fa + y.w * fb;
+    }
+  };
+  float* c_st = smem + 4 * C::state;   // KS = 4: the CTA's own state
+  for (int i = tid; i < n_tile * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    if (KS == 1 && S > 1) break;       // one state a row already
+    float mm, ll;
+    float4 x;
+    meet(KS, [&](int k, float2& ml, float4& y) {
+      const float* so = smem + (KS == 1 ? r >> 4 : k) * C::state;
+      ml = *reinterpret_cast<const float2*>(so + 16 * C::os + 2 * (r & 15));
+      y = *reinterpret_cast<const float4*>(so + (r & 15) * C::os + c);
+    }, mm, ll, x);
+    if (S == 1) {
+      finish(r, c, mm, ll, x);
+    } else {
+      *reinterpret_cast<float4*>(c_st + r * C::os + c) = x;
+      if (c == 0) *reinterpret_cast<float2*>(c_st + 16 * C::os + 2 * r) = make_float2(mm, ll);
+    }
+  }
+  if (S == 1) return;
+  tc::cluster_sync_all();
+  for (int i = rank * kThreads + tid; i < n_tile * (D / 4); i += S * kThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    const uint32_t so = tc::smem_addr(KS == 1 ? smem + (r >> 4) * C::state : c_st);
+    float mm, ll;
+    float4 x;
+    meet(S, [&](int k, float2& ml, float4& y) {
+      ml = tc::ld_cluster_v2(tc::mapa(so + 4u * (16 * C::os + 2 * (r & 15)), k));
+      y = tc::ld_cluster_v4(tc::mapa(so + 4u * ((r & 15) * C::os + c), k));
+    }, mm, ll, x);
+    finish(r, c, mm, ll, x);
   }
   tc::cluster_sync_all();   // no CTA leaves while its state may still be read
 }
 
-template <typename T, int D, int BM>
-cudaError_t launch_simt(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
-  const int rows = a.max_new * c.group;
-  const int tiles = (rows + BM - 1) / BM;
-  const long long items = (long long)tiles * c.cfg.n_kv_heads * a.batch;
-  // split the keys until two CTAs per SM, at least four key blocks each
+template <int D, int KS>
+cudaError_t launch_f32(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+  constexpr int BM = 64 / KS, kKeys = F32Cfg<D, KS>::keys, most = KS == 1 ? 8 : 16;
+  const int tiles = (a.max_new * c.group + BM - 1) / BM;
+  // CTAs that have rows, about; keys are split until four of them per SM, with
+  // at least four stages each
+  const long long packed = ((long long)a.n_tokens * c.group + BM - 1) / BM;
+  const int seqs = a.batch < a.n_tokens ? a.batch : a.n_tokens;
+  const long long busy = (packed > seqs ? packed : seqs) * c.cfg.n_kv_heads;
   int S = 1;
-  while (S < 8 && items * S < 2 * c.num_sms && (long long)a.max_len >= 2LL * S * 4 * kSimtKeys) S *= 2;
-  auto k = attend_simt_kernel<T, D, BM>;
-  constexpr size_t smem = SimtSmem<D, BM>::total;
+  while (S < most && busy * S < 4 * c.num_sms && (long long)a.max_len >= 2LL * S * 4 * kKeys) S *= 2;
+  const long long grid = (long long)tiles * a.batch * c.cfg.n_kv_heads * S;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  auto k = attend_f32_kernel<D, KS>;
+  constexpr int smem = F32Cfg<D, KS>::total;
   static std::atomic<uint64_t> attr_done{0};   // one bit per device
   const uint64_t bit = 1ull << (c.device & 63);
   if (!(attr_done.load() & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * S), c.cfg.n_kv_heads, a.batch);
-  cfg.blockDim = dim3(kSimtThreads, 1, 1);
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -289,9 +392,9 @@ cudaError_t launch_simt(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k, a, c.cfg.n_q_heads, c.group, S, tiles, c.err);
 }
 
-template <typename T, int D>
-cudaError_t launch_td(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
-  return a.max_new * c.group <= 16 ? launch_simt<T, D, 16>(c, a, st) : launch_simt<T, D, 64>(c, a, st);
+template <int D>
+cudaError_t launch_d(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+  return a.max_new * c.group <= 16 ? launch_f32<D, 4>(c, a, st) : launch_f32<D, 1>(c, a, st);
 }
 
 }  // namespace
@@ -299,7 +402,7 @@ cudaError_t launch_td(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
 cudaError_t launch_attend(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
   if (c.cfg.dtype == IMEM_BF16)
     return attend_step_fits(c, a) ? launch_attend_step(c, a, st) : launch_attend_tc(c, a, st);
-  return c.cfg.head_dim == 128 ? launch_td<float, 128>(c, a, st) : launch_td<float, 64>(c, a, st);
+  return c.cfg.head_dim == 128 ? launch_d<128>(c, a, st) : launch_d<64>(c, a, st);
 }
 
 }  // namespace imem
