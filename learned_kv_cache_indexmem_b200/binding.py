@@ -330,33 +330,40 @@ def set_rope(ctx, rope: Optional[Rope]) -> None:
            "imem_set_rope")
 
 
+# The calls below are made for every layer of a decode step, so their pointer
+# arguments are device addresses (ints) or None as they stand.
+
 def make_paged(k, v, block_table, kv_len, n_pages, page_size, max_pages) -> Paged:
-    return Paged(_ptr(k), _ptr(v), _ptr(block_table), _ptr(kv_len), n_pages, page_size, max_pages)
+    return Paged(k, v, block_table, kv_len, n_pages, page_size, max_pages)
 
 
 def rotate(ctx, n_tokens, positions, q, q_stride, q_out, q_out_stride, k, k_stride, k_out,
-           k_out_stride, inverse=False, stream=None):
-    _check(load().imem_rotate(
-        ctx, n_tokens, _ptr(positions), _ptr(q), q_stride, _ptr(q_out), q_out_stride, _ptr(k),
-        k_stride, _ptr(k_out), k_out_stride, int(inverse), _stream(stream)), "imem_rotate")
+           k_out_stride, inverse=0, stream=None):
+    code = load().imem_rotate(ctx, n_tokens, positions, q, q_stride, q_out, q_out_stride, k,
+                              k_stride, k_out, k_out_stride, inverse, _stream(stream))
+    if code:
+        raise IndexMemError(code, "imem_rotate")
 
 
 def append_paged(ctx, batch, n_tokens, tok_start, positions, k, k_stride, v, v_stride, q, q_stride,
                  q_out, q_out_stride, rotate, cache: Paged, stream=None):
-    _check(load().imem_append_paged(
-        ctx, batch, n_tokens, _ptr(tok_start), _ptr(positions), _ptr(k), k_stride, _ptr(v),
-        v_stride, _ptr(q), q_stride, _ptr(q_out), q_out_stride, int(rotate), cache,
-        _stream(stream)), "imem_append_paged")
+    code = load().imem_append_paged(ctx, batch, n_tokens, tok_start, positions, k, k_stride, v,
+                                    v_stride, q, q_stride, q_out, q_out_stride, rotate, cache,
+                                    _stream(stream))
+    if code:
+        raise IndexMemError(code, "imem_append_paged")
 
 
 def attend_paged(ctx, batch, n_tokens, tok_start, max_new, max_len, q, q_stride, cache: Paged,
                  scale, out, out_stride, lse, stream=None):
-    _check(load().imem_attend_paged(
-        ctx, batch, n_tokens, _ptr(tok_start), max_new, max_len, _ptr(q), q_stride, cache, scale,
-        _ptr(out), out_stride, _ptr(lse), _stream(stream)), "imem_attend_paged")
+    code = load().imem_attend_paged(ctx, batch, n_tokens, tok_start, max_new, max_len, q, q_stride,
+                                    cache, scale, out, out_stride, lse, _stream(stream))
+    if code:
+        raise IndexMemError(code, "imem_attend_paged")
 
 
 def gather_paged(ctx, batch, n, idx, idx_stride, cache: Paged, K, V, cap, stream=None):
-    _check(load().imem_gather_paged(
-        ctx, batch, n, _ptr(idx), idx_stride, cache, _ptr(K), _ptr(V), cap, _stream(stream)),
-        "imem_gather_paged")
+    code = load().imem_gather_paged(ctx, batch, n, idx, idx_stride, cache, K, V, cap,
+                                    _stream(stream))
+    if code:
+        raise IndexMemError(code, "imem_gather_paged")

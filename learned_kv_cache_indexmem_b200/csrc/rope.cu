@@ -27,8 +27,8 @@ namespace imem {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotTokens = 8;    // tokens per CTA (long calls)
-constexpr int kRotUnroll = 2;    // items in flight per thread
+constexpr int kRotTokens = 4;    // tokens per CTA (long calls; 8: 3 % slower)
+constexpr int kRotUnroll = 1;    // items in flight per thread (2: 15 % slower, fewer CTAs fit)
 
 template <typename T> struct Vec { static constexpr int n = 16 / sizeof(T); };
 

@@ -322,7 +322,9 @@ class IndexMemLayer:
             ks = self._tokens("k", k, T, self._hkv)
             k_out, kos = self._out("k_out", k_out, k, T, self._hkv)
         if T:
-            B_.rotate(self.ctx, T, positions, q, qs, q_out, qos, k, ks, k_out, kos, inverse, stream)
+            B_.rotate(self.ctx, T, positions.data_ptr(), q if q is None else q.data_ptr(), qs,
+                      q if q is None else q_out.data_ptr(), qos, k if k is None else k.data_ptr(),
+                      ks, k if k is None else k_out.data_ptr(), kos, 1 if inverse else 0, stream)
         return q_out, k_out
 
     def append_paged(self, k, v, cache: PagedCache, tok_start=None, positions=None, q=None,
@@ -345,8 +347,11 @@ class IndexMemLayer:
             qs = self._tokens("q", q, T, self._hq)
             q_out, qos = self._out("q_out", q_out, q, T, self._hq)
         if T:
-            B_.append_paged(self.ctx, b, T, tok_start, positions, k, ks, v, vs, q, qs, q_out, qos,
-                            rotate, pg, stream)
+            B_.append_paged(self.ctx, b, T, tok_start if tok_start is None else tok_start.data_ptr(),
+                            positions if positions is None else positions.data_ptr(), k.data_ptr(),
+                            ks, v.data_ptr(), vs, q if q is None else q.data_ptr(), qs,
+                            q if q is None else q_out.data_ptr(), qos, 1 if rotate else 0, pg,
+                            stream)
         return q_out
 
     def attend_paged(self, q, cache: PagedCache, tok_start=None, max_new: Optional[int] = None,
@@ -374,8 +379,9 @@ class IndexMemLayer:
         if max_len is None:
             max_len = min(pg.max_pages * pg.page_size, 2 ** 31 - 1)
         if T:
-            B_.attend_paged(self.ctx, b, T, tok_start, max_new, max_len, q, qs, pg,
-                            0.0 if scale is None else scale, out, os_, lse, stream)
+            B_.attend_paged(self.ctx, b, T, tok_start if tok_start is None else tok_start.data_ptr(),
+                            max_new, max_len, q.data_ptr(), qs, pg, 0.0 if scale is None else scale,
+                            out.data_ptr(), os_, lse if lse is None else lse.data_ptr(), stream)
         return (out, lse) if return_lse else out
 
     def gather_paged(self, cache: PagedCache, idx=None, n: Optional[int] = None, K=None, V=None,
@@ -400,7 +406,8 @@ class IndexMemLayer:
             raise ValueError("K and V must be contiguous %s [%d, >= %d, %d, %d] on %s" % (
                 (self.torch_dtype, b, n) + tail + (self._device,)))
         if n:
-            B_.gather_paged(self.ctx, b, n, idx, n, pg, K, V, K.shape[1], stream)
+            B_.gather_paged(self.ctx, b, n, idx if idx is None else idx.data_ptr(), n, pg,
+                            K.data_ptr(), V.data_ptr(), K.shape[1], stream)
         return K, V
 
     def evict_paged(self, X, Q, cache: PagedCache, st: PrefillState, B: int, chunk: int = 512,
