@@ -10,10 +10,12 @@
 // but O, m and l stays in registers between tiles.
 //
 // A CTA streams its share of a sequence's keys in stages of 64 through a ring
-// that one producer warp fills by TMA, page by page; each of four warps takes 16 keys of
-// every stage with a softmax state of its own (no block barrier in the loop;
-// 96 KB of ring, two CTAs per SM, so that one's start and end hide behind the
-// other's stream). The CTAs of a sequence and KV head form a cluster; their
+// that one producer warp fills by TMA, page by page. Two pairs of warps take
+// the stages in turn, each warp 32 keys of its pair's with a softmax state of
+// its own: two independent tiles per warp hide the MMAs' latency (one tile of
+// 16 keys of every stage per warp: 1.3 us a stage with 20 rows), and no
+// block barrier is in the loop. 96 KB of ring, two CTAs per SM, so that one's
+// start and end hide behind the other's stream. The CTAs of a sequence and KV head form a cluster; their
 // warps' states meet over distributed shared memory at the end.
 #include "common.cuh"
 #include "internal.h"
@@ -188,53 +190,72 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
 #pragma unroll
       for (int e = 0; e < 2; ++e) pos[nt][e] = past + min(8 * nt + 2 * t + e, n_rows - 1) / G;
 
-    const int kr = warp * 16 + (lane & 15);                    // ldmatrix row of K
-    const int vr = warp * 16 + (lane & 7) + (lane >> 4) * 8;   // of V
+    const int w0 = (warp & 1) * 32;                        // the warp's keys of a stage
+    const int kr = w0 + (lane & 15);                       // ldmatrix row of K
+    const int vr = w0 + (lane & 7) + (lane >> 4) * 8;      // of V
     for (int j = 0; j < n; ++j) {
       const int st = j % C::stages;
       const uint32_t kt = sR + st * 2 * C::tile, vt = kt + C::tile;
+      // every warp sees every phase of a stage's barriers: one that left out
+      // the other pair's would take the phase before it for the next one
       if (!tc::mbar_wait(full + 8 * st, (j / C::stages) & 1)) {
         record_error(err, DEV_TIMEOUT);
         break;
       }
-      const int key0 = (b0 + j) * kRows + warp * 16;
-      if (key0 + 16 > n_keys) {
+      if ((j & 1) != warp >> 1) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(empty + 8 * st);
+        continue;
+      }
+      const int key0 = (b0 + j) * kRows + w0;
+      if (key0 + 32 > n_keys) {
         // value rows that no row sees: whatever is there must not reach O
-        for (int i = lane; i < 16 * (D / 8); i += 32) {
-          const int r = warp * 16 + i / (D / 8), c = i % (D / 8);
+        for (int i = lane; i < 32 * (D / 8); i += 32) {
+          const int r = w0 + i / (D / 8), c = i % (D / 8);
           if (key0 + i / (D / 8) >= n_keys)
             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(
                              vt + (c >> 3) * C::half + r * 128 + (c & 7) * 16), "r"(0u) : "memory");
         }
         __syncwarp();
       }
-      // scores: keys g and g + 8 of the tile, rows 2 t and 2 t + 1
-      float s[NT][4], s2[NT][4];
+      // scores of two tiles of 16 keys: keys g and g + 8 of a tile, rows 2 t
+      // and 2 t + 1; two chains of products each
+      float s[2][NT][4], s2[2][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = s2[nt][0] = s2[nt][1] = s2[nt][2] = s2[nt][3] = 0.f;
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int k = 0; k < D / 16; k += 2) {   // two chains of products per score
-        uint32_t af[2][4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int c = 2 * (k + u) + (lane >> 4);
-          ldsm4(kt + (c >> 3) * C::half + kr * 128 + (((c & 7) ^ (kr & 7)) << 4), af[u]);
-        }
+          for (int e = 0; e < 4; ++e) s[x][nt][e] = s2[x][nt][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; k += 2) {
+        uint32_t af[2][2][4], qb[NT][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int c = 2 * (k + u) + (lane >> 4);
+            ldsm4(kt + (c >> 3) * C::half + (kr + 16 * x) * 128 + (((c & 7) ^ (kr & 7)) << 4), af[x][u]);
+          }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (C::q_smem) {
-            uint32_t b[4];   // chunks 2 k .. 2 k + 3 of rows 8 nt ..
-            ldsm4(sR + C::q + (8 * nt + (lane & 7)) * C::q_row + (2 * k + (lane >> 3)) * 16, b);
-            mma16(s[nt], af[0], b[0], b[1]);
-            mma16(s2[nt], af[1], b[2], b[3]);
+          if constexpr (C::q_smem) {   // chunks 2 k .. 2 k + 3 of rows 8 nt ..
+            ldsm4(sR + C::q + (8 * nt + (lane & 7)) * C::q_row + (2 * k + (lane >> 3)) * 16, qb[nt]);
           } else {
-            mma16(s[nt], af[0], q0[nt][k], q1[nt][k]);
-            mma16(s2[nt], af[1], q0[nt][k + 1], q1[nt][k + 1]);
+            qb[nt][0] = q0[nt][k]; qb[nt][1] = q1[nt][k];
+            qb[nt][2] = q0[nt][k + 1]; qb[nt][3] = q1[nt][k + 1];
           }
         }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16(s[x][nt], af[x][0], qb[nt][0], qb[nt][1]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16(NT == 3 ? s[x][nt] : s2[x][nt], af[x][1], qb[nt][2], qb[nt][3]);
       }
-      uint32_t p0[NT], p1[NT];
+      uint32_t p[2][NT][2];
       float f[NT][2];
       bool any = false;
 #pragma unroll
@@ -242,9 +263,15 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
         float mx[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          s[nt][e] = key0 + g <= pos[nt][e] ? s[nt][e] + s2[nt][e] : -INFINITY;
-          s[nt][2 + e] = key0 + g + 8 <= pos[nt][e] ? s[nt][2 + e] + s2[nt][2 + e] : -INFINITY;
-          mx[e] = fmaxf(s[nt][e], s[nt][2 + e]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int key = key0 + 16 * x + g;
+            float &a0 = s[x][nt][e], &a1 = s[x][nt][2 + e];
+            if (NT != 3) { a0 += s2[x][nt][e]; a1 += s2[x][nt][2 + e]; }
+            a0 = key <= pos[nt][e] ? a0 : -INFINITY;
+            a1 = key + 8 <= pos[nt][e] ? a1 : -INFINITY;
+          }
+          mx[e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
         }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
@@ -258,14 +285,22 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
           if (grown) m[nt][e] = mx[e];
           any |= grown;
           const float nm = m[nt][e] == -INFINITY ? 0.f : -m[nt][e] * sl2;
-          s[nt][e] = tc::ex2(fmaf(s[nt][e], sl2, nm));
-          s[nt][2 + e] = tc::ex2(fmaf(s[nt][2 + e], sl2, nm));
-          l[nt][e] = l[nt][e] * f[nt][e] + (s[nt][e] + s[nt][2 + e]);
+          float sum = 0.f;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            s[x][nt][e] = tc::ex2(fmaf(s[x][nt][e], sl2, nm));
+            s[x][nt][2 + e] = tc::ex2(fmaf(s[x][nt][2 + e], sl2, nm));
+            sum += s[x][nt][e] + s[x][nt][2 + e];
+          }
+          l[nt][e] = l[nt][e] * f[nt][e] + sum;
         }
-        const __nv_bfloat162 a0 = __floats2bfloat162_rn(s[nt][0], s[nt][1]);
-        const __nv_bfloat162 a1 = __floats2bfloat162_rn(s[nt][2], s[nt][3]);
-        p0[nt] = transpose8(*reinterpret_cast<const uint32_t*>(&a0));
-        p1[nt] = transpose8(*reinterpret_cast<const uint32_t*>(&a1));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const __nv_bfloat162 a0 = __floats2bfloat162_rn(s[x][nt][0], s[x][nt][1]);
+          const __nv_bfloat162 a1 = __floats2bfloat162_rn(s[x][nt][2], s[x][nt][3]);
+          p[x][nt][0] = transpose8(*reinterpret_cast<const uint32_t*>(&a0));
+          p[x][nt][1] = transpose8(*reinterpret_cast<const uint32_t*>(&a1));
+        }
       }
       if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
@@ -277,13 +312,15 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
           }
       }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int c = 2 * i + ((lane >> 3) & 1);
-        uint32_t af[4];
-        ldsm4_t(vt + (c >> 3) * C::half + vr * 128 + (((c & 7) ^ (vr & 7)) << 4), af);
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16(o[nt][i], af, p0[nt], p1[nt]);
-      }
+        for (int i = 0; i < D / 16; ++i) {
+          const int c = 2 * i + ((lane >> 3) & 1);
+          uint32_t af[4];
+          ldsm4_t(vt + (c >> 3) * C::half + (vr + 16 * x) * 128 + (((c & 7) ^ (vr & 7)) << 4), af);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16(o[nt][i], af, p[x][nt][0], p[x][nt][1]);
+        }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(empty + 8 * st);
     }

@@ -274,6 +274,10 @@ CASES = [
     ("bf16", 128, 8, 1, 256, [129], [700]),
     ("bf16", 64, 2, 1, 64, [128, 127], [128, 2000]),
     ("bf16", 128, 2, 2, 512, [513, 255], [520, 255]),
+    ("bf16", 128, 8, 2, 16, [1, 1, 1], [9000, 12001, 30000]),     # many turns of the ring
+    ("bf16", 64, 8, 2, 64, [2, 5], [20001, 9000]),
+    ("bf16", 128, 16, 8, 32, [12, 11], [7000, 5001]),
+    ("bf16", 64, 8, 2, 32, [70, 3], [9000, 11]),
     ("fp32", 64, 8, 2, 16, [1, 1], [1, 1030]),
     ("fp32", 128, 8, 2, 64, [1], [5000]),
     ("fp32", 64, 8, 2, 16, [100, 1, 0, 31], [100, 400, 5, 90]),
