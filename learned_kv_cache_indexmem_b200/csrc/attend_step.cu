@@ -123,16 +123,16 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     // the table entries of 32 boxes at a time, one per lane: a stage's boxes
     // then cost a shuffle instead of a load's latency
     const int boxes = (n * kRows + box - 1) / box;
-    int pids = -2;
+    int pids = -1;
     for (int j = 0; j < n; ++j) {
       const int first = j * parts;
       if ((first & 31) == 0) {
         const int i = first + lane, key = b0 * kRows + i * box;
-        pids = i < boxes && key < n_keys ? table[key >> a.pg.page_log] : -2;
+        pids = i < boxes && key < n_keys ? table[key >> a.pg.page_log] : -1;
       }
       const int pid = __shfl_sync(0xffffffffu, pids, (first + (lane < parts ? lane : 0)) & 31);
       const bool load = lane < parts && pid >= 0 && pid < a.pg.n_pages;
-      if (lane < parts && pid != -2 && !load) record_error(err, DEV_RANGE);
+      if (lane < parts && (b0 + j) * kRows + lane * box < n_keys && !load) record_error(err, DEV_RANGE);
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (D * 4);
       const int st = j % C::stages;
       if (j >= C::stages && !tc::mbar_wait(empty + 8 * st, (j / C::stages - 1) & 1)) {
@@ -444,7 +444,7 @@ int step_splits(const Ctx& c, const AttendArgs& a, const int (&resident)[17]) {
   }
   long long S = (4LL * resident[1] + units - 1) / units;
   if (S > a.max_len / 1024) S = a.max_len / 1024;
-  return S < 1 ? 1 : S > 16 ? 16 : (int)S;
+  return S < 1 ? 1 : S > 8 ? 8 : (int)S;
 }
 
 template <int D, int NT>

@@ -185,9 +185,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tc::tma_load_3d(sQ + t * C::tile + c * C::half, &mq, q_full, 64 * c, h * G,
                             sq.tok0 + (r0 + t * 128) / G);
       }
-      auto page_of = [&](int j) {   // this lane's box of key tile j
-        const int key = (b0 + j) * kKeys + lane * box;
-        return j < n && lane < parts && key < n_keys ? table[key >> a.pg.page_log] : -2;
+      auto needs = [&](int j) {   // this lane has a box of key tile j
+        return j < n && lane < parts && (b0 + j) * kKeys + lane * box < n_keys;
+      };
+      auto page_of = [&](int j) {
+        return needs(j) ? table[((b0 + j) * kKeys + lane * box) >> a.pg.page_log] : -1;
       };
       int next = page_of(0);
       bool ok = true;
@@ -195,7 +197,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const int pid = next;
         next = page_of(j + 1);
         const bool load = pid >= 0 && pid < a.pg.n_pages;
-        if (pid != -2 && !load) record_error(err, DEV_RANGE);
+        if (needs(j) && !load) record_error(err, DEV_RANGE);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (D * 2);
         const int y = (pid << a.pg.page_log) + (((b0 + j) * kKeys) & (page - 1) & ~(box - 1));
         for (int v = 0; v < 2; ++v) {

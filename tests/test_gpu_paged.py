@@ -227,7 +227,7 @@ def test_append_padding_in_front_and_bad_pages(cuda_device):
         if bad == "page":
             bt.cache.block_table[1, 2] = bt.cache.K.shape[0]
         elif bad == "page-":
-            bt.cache.block_table[1, 2] = -5
+            bt.cache.block_table[1, 2] = -2
         elif bad == "len":
             bt.cache.kv_len[1] = 16 * bt.cache.block_table.shape[1] + 1
         else:
@@ -278,6 +278,8 @@ CASES = [
     ("bf16", 64, 8, 2, 64, [2, 5], [20001, 9000]),
     ("bf16", 128, 16, 8, 32, [12, 11], [7000, 5001]),
     ("bf16", 64, 8, 2, 32, [70, 3], [9000, 11]),
+    ("bf16", 128, 8, 1, 16, [4], [40]),                           # fewer tokens than a tile has rows
+    ("bf16", 64, 2, 2, 16, [25], [25]),
     ("fp32", 64, 8, 2, 16, [1, 1], [1, 1030]),
     ("fp32", 128, 8, 2, 64, [1], [5000]),
     ("fp32", 64, 8, 2, 16, [100, 1, 0, 31], [100, 400, 5, 90]),
@@ -333,6 +335,59 @@ def test_attend_large_logits_and_infinite_stale_rows(cuda_device, dtype):
                 lay.sync()
             assert ei.value.name == "IMEM_ERR_RANGE"
         lay.close()
+
+
+@pytest.mark.parametrize("dtype,new", [("bf16", 6), ("bf16", 60), ("fp32", 3), ("fp32", 60)])
+def test_attend_reports_bad_pages(cuda_device, dtype, new):
+    lay = layer(cuda_device, dtype=dtype)
+    for value in (-1, -2, -(1 << 31), 1 << 30, None):
+        bt = batch(cuda_device, [new, new], [200, 500], dtype=dtype)
+        good = lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=new)
+        lay.sync()
+        bt.cache.block_table[1, 30] = bt.cache.K.shape[0] if value is None else value
+        out = lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=new)
+        with pytest.raises(B.IndexMemError) as ei:
+            lay.sync()
+        assert ei.value.name == "IMEM_ERR_RANGE"
+        assert torch.equal(out[:new], good[:new])          # the other sequence
+    lay.close()
+
+
+def test_caches_past_32_bit_offsets(cuda_device):
+    """Pages whose rows lie more than 2^32 bytes and 2^31 elements into the cache."""
+    hq, hkv, d, page = 8, 8, 128, 64
+    n_pages = (1 << 31) // (page * hkv * d) + 40
+    for dtype, new in (("bf16", 1), ("bf16", 40), ("fp32", 5)):
+        lay = layer(cuda_device, hq, hkv, d, dtype)
+        dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+        cache = lay.new_paged(2, n_pages, page, 4, cuda_device)
+        table = torch.tensor([[n_pages - 1, 3, n_pages - 7, 0], [n_pages - 20, n_pages - 21, 1, 2]])
+        cache.block_table.copy_(table.to(torch.int32))
+        lens = [250, 130]
+        for s in range(2):
+            cache.K[table[s].to(cuda_device)] = torch.randn(4, page, hkv, d, device=cuda_device).to(dt)
+            cache.V[table[s].to(cuda_device)] = torch.randn(4, page, hkv, d, device=cuda_device).to(dt)
+        cache.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        q, k, v = (torch.randn(2 * new, h, d, device=cuda_device).to(dt) for h in (hq, hkv, hkv))
+        qr = lay.append_paged(k, v, cache, q=q)
+        out, lse = lay.attend_paged(qr, cache, return_lse=True)
+        K, V = lay.gather_paged(cache, n=130)
+        lay.sync()
+        # the same cache, its pages moved to the front
+        ids = table.flatten().tolist()
+        small = PagedCache(torch.stack([cache.K[i] for i in ids]), torch.stack([cache.V[i] for i in ids]),
+                           torch.arange(8, dtype=torch.int32, device=cuda_device).view(2, 4), cache.kv_len)
+        bt = Batch(qr, None, None, torch.tensor([0, new, 2 * new], dtype=torch.int32), small, [new, new], lens, None)
+        check_attend(out, lse, bt, None)
+        for s in range(2):
+            rows = po.slots(small.block_table[s].tolist(), page, lens[s])
+            at = torch.from_numpy(rows).to(cuda_device)
+            pos = np.arange(lens[s] - new, lens[s])
+            check_rotated(small.K.view(-1, hkv, d)[at[-new:]], k[s * new:(s + 1) * new], pos, po.frequencies(d, 500000.0), "half")
+            assert torch.equal(small.V.view(-1, hkv, d)[at[-new:]], v[s * new:(s + 1) * new])
+            assert torch.equal(K[s], small.K.view(-1, hkv, d)[at[:130]]) and torch.equal(V[s], small.V.view(-1, hkv, d)[at[:130]])
+        lay.close()
+        del cache
 
 
 def test_attend_non_finite_values_reach_only_who_may_see_them(cuda_device):
