@@ -542,9 +542,11 @@ imem_status imem_append_paged(imem_ctx* ctx, int batch, int n_tokens, const int3
  *   lse = ln sum_{j <= p} exp(s_j)            (fp32 [n_tokens, Hq], or NULL)
  * A token that sees no key (p < 0) gets out = 0 and lse = -inf. Keys and values
  * past kv_len are never used, whatever the pages hold there. Within a chunk a
- * value row that is not finite may also reach the outputs of the up to 127
- * tokens before it. softmax in fp32; bf16: probabilities are rounded to bf16
- * for the product with V, as imem_decode does.
+ * value row that is not finite may also reach the outputs of the 255 tokens
+ * before it (0 * inf in a masked place of their tile). softmax in fp32; bf16:
+ * probabilities are rounded to bf16 for the product with V, as imem_decode
+ * does; fp32: products from two tf32 halves, about fp32's own accuracy. out
+ * must not overlap q or the cache.
  * scale > 0 and finite; 0: 1/sqrt(d).
  * max_new: no sequence has more new tokens (<= n_tokens; one that has more is
  * reported as RANGE and its tokens past max_new are not computed). max_len: the

@@ -3,16 +3,19 @@
 //
 //   s_ij = scale q_i . k_j,  o_i = sum_{j <= p_i} softmax(s_i)_j v_j
 //
-// fp32 products on the tensor cores. A value is split into hi (its upper 11
-// significant bits, the operand format tf32) and lo = x - hi (exact; its upper
-// 11 bits are kept), and a product becomes hi hi + hi lo + lo hi with fp32
-// accumulation: what is dropped is below 3 * 2^-22 of |x y|, next to the 2^-24
-// per addition that any fp32 sum of d products rounds by. Bound by the
-// warp-level MMA: one m16n8k8 (tf32) or m16n8k16 (bf16) per 16 clocks and SM
-// quarter, so three tf32 products cost half of what six bf16 ones of a
-// three-way split do per value, and both beat the fp32 units as far as shared
-// memory feeds those (1024 new tokens, 8 heads of 64: 56 us on them, 47-51
-// us with three bf16 parts, 40 us here; 46 TFLOP/s at 8192 keys).
+// fp32 products on the tensor cores. A value is split into hi (rounded to the
+// operand format tf32, 11 significant bits) and lo = x - hi (exact, of either
+// sign; its upper 11 bits are kept), and a product becomes hi hi + hi lo +
+// lo hi with fp32 accumulation: what is dropped is below 2^-22 of |x y|. The
+// unit cuts its sums off instead of rounding them, which over many keys
+// would pull every sum towards zero, so that only short chains stay inside it
+// (16 dimensions, one stage of keys) and meet by rounded additions: 1.6e-6
+// off the exact outputs without that, for 1024 keys. Bound by the warp-level
+// MMA: one m16n8k8 (tf32) or m16n8k16 (bf16) per 16 clocks and SM quarter, so
+// three tf32 products cost as much as six bf16 ones of a three-way split with
+// less arithmetic around them, and both beat the fp32 units as far as shared
+// memory feeds those (1024 new tokens, 8 heads of 64: 44 us, 25 TFLOP/s; on
+// the fp32 units 56 us).
 //
 // A tile's rows are the new tokens of one sequence times the G query heads of
 // one KV head (row r: token r / G, head r % G), so that K and V are read once
@@ -55,9 +58,9 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool valid)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(tc::smem_addr(dst)),
                "l"(src), "r"(valid ? 16 : 0) : "memory");   // 0: zero-filled
 }
-// x = hi + lo, hi with 11 significant bits
+// x = hi + lo, hi the nearest value of 11 significant bits
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;   // (cvt.rna: 48 against 44 us)
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 // C (16 x 8) += A (16 x 8) B (8 x 8), tf32 operands
@@ -191,15 +194,22 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
       }
       // one product of every tile before the next: a dependent MMA waits for
       // its accumulator several times as long as the unit takes for it
+      float part[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) part[i][0] = part[i][1] = part[i][2] = part[i][3] = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) mma8(lo[i], al[k], bh[i][2 * k], bh[i][2 * k + 1]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) mma8(s[i], ah[k], bh[i][2 * k], bh[i][2 * k + 1]);
+        for (int i = 0; i < NT; ++i) mma8(part[i], ah[k], bh[i][2 * k], bh[i][2 * k + 1]);
 #pragma unroll
         for (int i = 0; i < NT; ++i) mma8(lo[i], ah[k], bl[i][2 * k], bl[i][2 * k + 1]);
       }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] += part[i][e];
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -241,16 +251,22 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
         o[i][0] *= f[0]; o[i][1] *= f[0]; o[i][2] *= f[1]; o[i][3] *= f[1];
       }
     }
+    // step i: index t is key 8 i + 2 t, index t + 4 the key after it
+    uint32_t ph[NT][4], pl[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      // step i: index t is key 8 i + 2 t, index t + 4 the key after it
-      uint32_t ah[4], al[4];
-      split(s[i][0], ah[0], al[0]);
-      split(s[i][2], ah[1], al[1]);
-      split(s[i][1], ah[2], al[2]);
-      split(s[i][3], ah[3], al[3]);
+      split(s[i][0], ph[i][0], pl[i][0]);
+      split(s[i][2], ph[i][1], pl[i][1]);
+      split(s[i][1], ph[i][2], pl[i][2]);
+      split(s[i][3], ph[i][3], pl[i][3]);
+    }
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+    for (int c = 0; c < D / 32; ++c) {
+      float part[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) part[k][0] = part[k][1] = part[k][2] = part[k][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
         const float4 x = *reinterpret_cast<const float4*>(vb + 8 * i * C::vs + 32 * c);
         const float4 y = *reinterpret_cast<const float4*>(vb + (8 * i + 1) * C::vs + 32 * c);
         const float v[2][4] = {{x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}};
@@ -261,12 +277,16 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
           split(v[1][k], vh[1][k], vl[1][k]);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma8(o[4 * c + k], al, vh[0][k], vh[1][k]);
+        for (int k = 0; k < 4; ++k) mma8(part[k], pl[i], vh[0][k], vh[1][k]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma8(o[4 * c + k], ah, vl[0][k], vl[1][k]);
+        for (int k = 0; k < 4; ++k) mma8(part[k], ph[i], vl[0][k], vl[1][k]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma8(o[4 * c + k], ah, vh[0][k], vh[1][k]);
+        for (int k = 0; k < 4; ++k) mma8(part[k], ph[i], vh[0][k], vh[1][k]);
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[4 * c + k][e] += part[k][e];
     }
     __syncthreads();   // the buffer may be filled again
   }
