@@ -28,7 +28,6 @@ namespace {
 
 constexpr int kRotThreads = 256;
 constexpr int kRotTokens = 4;    // tokens per CTA (long calls; 8: 3 % slower)
-constexpr int kRotUnroll = 1;    // items in flight per thread (2: 15 % slower, fewer CTAs fit)
 
 template <typename T> struct Vec { static constexpr int n = 16 / sizeof(T); };
 
@@ -66,13 +65,16 @@ struct Item {
   bool turn;
 };
 
-// kPaged: append (k and v go to the cache rows of tok). D: head dimension.
+// kPaged: append (k and v go to cache rows). D: head dimension. by_per:
+// ceil(2^32 / items per token), which divides item numbers (below 2^16) by it.
 template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(kRotThreads)
 rotate_kernel(const __grid_constant__ RotateArgs a, const __grid_constant__ RopeTable rope, int Hq,
-              int Hkv, int tokens, int* __restrict__ err) {
+              int Hkv, int tokens, uint32_t by_per, int* __restrict__ err) {
   constexpr int V = Vec<T>::n;
   constexpr int IPH = D / (2 * V);        // items per head
+  // pair f = j V + e at [e (64 / V) + j]: lanes of neighbouring items read side by side
+  constexpr int VS = 64 / V;
   __shared__ float2 s_cs[kRotTokens][64];
   __shared__ long long s_row[kRotTokens];  // cache row, -1: token skipped
   __shared__ int s_pos[kRotTokens];
@@ -87,7 +89,7 @@ rotate_kernel(const __grid_constant__ RotateArgs a, const __grid_constant__ Rope
 
   auto item = [&](int i) {
     Item it;
-    it.token = i / per;
+    it.token = __umulhi(i, by_per);
     const int r = i - it.token * per;
     it.head = r / IPH;
     const int j = r - it.head * IPH;
@@ -113,21 +115,15 @@ rotate_kernel(const __grid_constant__ RotateArgs a, const __grid_constant__ Rope
     return (const T*)a.v + t * a.v_stride + (it.head - nq - nk) * D;
   };
 
-  // the first items' loads need nothing of what follows
-  uint4 x0[kRotUnroll], x1[kRotUnroll];
-  auto load = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < kRotUnroll; ++u) {
-      const int i = base + u * kRotThreads + tid;
-      if (i < total) {
-        const Item it = item(i);
-        const T* p = source(it);
-        x0[u] = *reinterpret_cast<const uint4*>(p + it.src0);
-        x1[u] = *reinterpret_cast<const uint4*>(p + it.src1);
-      }
-    }
+  // the first item's loads need nothing of what follows (two items in flight
+  // per thread: 15 % slower, fewer CTAs fit)
+  uint4 x0, x1;
+  auto load = [&](const Item& it) {
+    const T* p = source(it);
+    x0 = *reinterpret_cast<const uint4*>(p + it.src0);
+    x1 = *reinterpret_cast<const uint4*>(p + it.src1);
   };
-  load(0);
+  if (tid < total) load(item(tid));
 
   // positions and, for append, cache rows: one warp per token
   for (int k = tid >> 5; k < nt; k += kRotThreads / 32) {
@@ -173,59 +169,54 @@ rotate_kernel(const __grid_constant__ RotateArgs a, const __grid_constant__ Rope
       const float x = (float)(int32_t)(phase >> 32) * 0x1p-31f;   // half turns in [-1, 1)
       float sn, cs;
       sincospif(x, &sn, &cs);
-      s_cs[k][f] = make_float2(cs * rope.magnitude, (a.inverse ? -sn : sn) * rope.magnitude);
+      s_cs[k][f % V * VS + f / V] = make_float2(cs * rope.magnitude, (a.inverse ? -sn : sn) * rope.magnitude);
     }
     __syncthreads();
   }
 
-  for (int base = 0; base < total; base += kRotUnroll * kRotThreads) {
-    if (base) load(base);
+  for (int i = tid; i < total; i += kRotThreads) {
+    const Item it = item(i);
+    if (i != tid) load(it);
+    if (kPaged && s_row[it.token] < 0) continue;
+    if (it.turn) {
+      float f0[V], f1[V];
+      unpack<T>(x0, f0);
+      unpack<T>(x1, f1);
+      if (rope.interleaved) {
+        const float2* cs = &s_cs[it.token][it.src0 / (2 * V)];
 #pragma unroll
-    for (int u = 0; u < kRotUnroll; ++u) {
-      const int i = base + u * kRotThreads + tid;
-      if (i >= total) break;
-      const Item it = item(i);
-      if (kPaged && s_row[it.token] < 0) continue;
-      if (it.turn) {
-        float f0[V], f1[V];
-        unpack<T>(x0[u], f0);
-        unpack<T>(x1[u], f1);
-        if (rope.interleaved) {
-          const float2* cs = &s_cs[it.token][it.src0 >> 1];
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            const float2 p = cs[e], q = cs[V / 2 + e];
-            const float a0 = f0[2 * e], b0 = f0[2 * e + 1], a1 = f1[2 * e], b1 = f1[2 * e + 1];
-            f0[2 * e] = a0 * p.x - b0 * p.y;
-            f0[2 * e + 1] = b0 * p.x + a0 * p.y;
-            f1[2 * e] = a1 * q.x - b1 * q.y;
-            f1[2 * e + 1] = b1 * q.x + a1 * q.y;
-          }
-        } else {
-          const float2* cs = &s_cs[it.token][it.src0];
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float2 p = cs[e];
-            const float a0 = f0[e], b0 = f1[e];
-            f0[e] = a0 * p.x - b0 * p.y;
-            f1[e] = b0 * p.x + a0 * p.y;
-          }
+        for (int e = 0; e < V / 2; ++e) {
+          const float2 p = cs[e * VS], q = cs[(V / 2 + e) * VS];
+          const float a0 = f0[2 * e], b0 = f0[2 * e + 1], a1 = f1[2 * e], b1 = f1[2 * e + 1];
+          f0[2 * e] = a0 * p.x - b0 * p.y;
+          f0[2 * e + 1] = b0 * p.x + a0 * p.y;
+          f1[2 * e] = a1 * q.x - b1 * q.y;
+          f1[2 * e + 1] = b1 * q.x + a1 * q.y;
         }
-        x0[u] = pack<T>(f0);
-        x1[u] = pack<T>(f1);
-      }
-      const long long t = t0 + it.token;
-      T* p;
-      if (it.kind == 0) p = (T*)a.q_out + t * a.q_out_stride + it.head * D;
-      else if (kPaged) {
-        const int h = it.kind == 1 ? it.head - nq : it.head - nq - nk;
-        p = (T*)(it.kind == 1 ? a.pg.k : a.pg.v) + (s_row[it.token] * Hkv + h) * D;
       } else {
-        p = (T*)a.k_out + t * a.k_out_stride + (it.head - nq) * D;
+        const float2* cs = &s_cs[it.token][it.src0 / V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float2 p = cs[e * VS];
+          const float a0 = f0[e], b0 = f1[e];
+          f0[e] = a0 * p.x - b0 * p.y;
+          f1[e] = b0 * p.x + a0 * p.y;
+        }
       }
-      *reinterpret_cast<uint4*>(p + it.src0) = x0[u];
-      *reinterpret_cast<uint4*>(p + it.src1) = x1[u];
+      x0 = pack<T>(f0);
+      x1 = pack<T>(f1);
     }
+    const long long t = t0 + it.token;
+    T* p;
+    if (it.kind == 0) p = (T*)a.q_out + t * a.q_out_stride + it.head * D;
+    else if (kPaged) {
+      const int h = it.kind == 1 ? it.head - nq : it.head - nq - nk;
+      p = (T*)(it.kind == 1 ? a.pg.k : a.pg.v) + (s_row[it.token] * Hkv + h) * D;
+    } else {
+      p = (T*)a.k_out + t * a.k_out_stride + (it.head - nq) * D;
+    }
+    *reinterpret_cast<uint4*>(p + it.src0) = x0;
+    *reinterpret_cast<uint4*>(p + it.src1) = x1;
   }
 }
 
@@ -236,12 +227,13 @@ cudaError_t launch_td(const Ctx& c, const RotateArgs& a, cudaStream_t st) {
   const int tokens = a.n_tokens >= 2 * kRotTokens * c.num_sms ? kRotTokens
                      : a.n_tokens > 2 * c.num_sms ? 2 : 1;
   const int grid = (a.n_tokens + tokens - 1) / tokens;
+  const int Hq = c.cfg.n_q_heads, Hkv = c.cfg.n_kv_heads;
+  const uint32_t per = ((a.q ? Hq : 0) + (a.k ? Hkv : 0) + (a.pg.k ? Hkv : 0)) * (D * sizeof(T) / 32);
+  const uint32_t by_per = 0xffffffffu / per + 1;
   if (a.pg.k)
-    rotate_kernel<T, D, true><<<grid, kRotThreads, 0, st>>>(a, c.rope, c.cfg.n_q_heads,
-                                                            c.cfg.n_kv_heads, tokens, c.err);
+    rotate_kernel<T, D, true><<<grid, kRotThreads, 0, st>>>(a, c.rope, Hq, Hkv, tokens, by_per, c.err);
   else
-    rotate_kernel<T, D, false><<<grid, kRotThreads, 0, st>>>(a, c.rope, c.cfg.n_q_heads,
-                                                             c.cfg.n_kv_heads, tokens, c.err);
+    rotate_kernel<T, D, false><<<grid, kRotThreads, 0, st>>>(a, c.rope, Hq, Hkv, tokens, by_per, c.err);
   return cudaGetLastError();
 }
 
