@@ -415,10 +415,12 @@ class IndexMemLayer:
         """From a paged prompt to the decode state: scores the prompt's hidden
         states X [b, L, H] and queries Q [b, L, Hq, d], keeps the B most
         important of its L cached tokens in st's retained cache and adds the
-        others to the memory. Every sequence holds L tokens; the pages are free
-        to be reused once the stream has passed this call."""
-        L = X.shape[1]
-        K, V = self.gather_paged(cache, n=L, stream=stream)
+        others to the memory. Every sequence holds L tokens (a shorter one is
+        reported by sync as IMEM_ERR_RANGE); the pages are free to be reused
+        once the stream has passed this call."""
+        b, L = X.shape[0], X.shape[1]
+        at = torch.arange(L, dtype=torch.int32, device=X.device).expand(b, L).contiguous()
+        K, V = self.gather_paged(cache, at, stream=stream)
         self.score_and_evict(X, Q, K, V, st, B, stream=stream)
         self.update_memory(K, V, st, B, chunk=chunk, stream=stream)
 

@@ -577,6 +577,24 @@ def test_chunks_through_the_pages_match_one_prompt(cuda_device, dtype, d):
         l_.close()
 
 
+def test_readme_paged_example_runs(cuda_device):
+    """The README's second example, after its first (whose layer stays open)."""
+    import pathlib
+    import re
+    text = (pathlib.Path(__file__).resolve().parent.parent / "README.md").read_text()
+    first, second = re.findall(r"```python\n(.*?)```", text, re.S)[:2]
+    ns: dict = {}
+    exec(compile(first.replace("layer.close()", ""), "README.md", "exec"), ns)
+    exec(compile(second, "README.md", "exec"), ns)
+    assert ns["o"].shape == ns["dec"]["q"][0].shape and torch.isfinite(ns["o"].float()).all()
+    ns["pages"].kv_len.fill_(4000)          # shorter than the prompt: reported
+    ns["layer"].evict_paged(ns["x"]["X"], ns["q_rot"], ns["pages"], ns["st"], ns["B"])
+    with pytest.raises(B.IndexMemError) as ei:
+        ns["layer"].sync()
+    assert ei.value.name == "IMEM_ERR_RANGE"
+    ns["layer"].close()
+
+
 def test_paged_prompt_to_eviction_and_decode(cuda_device):
     """rotate + append + attend over pages, then the learned eviction out of the
     pages, the memory and decode steps, each stage against the oracle."""
