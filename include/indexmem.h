@@ -463,7 +463,7 @@ imem_status imem_decode_online(imem_ctx* ctx, int batch, int B, const void* x_ne
  * new tokens has position kv_len[s] - n + i. A negative position (a sequence
  * padded in front) is padding too: it is not appended and attends to nothing.
  * Table entries past the last page that kv_len reaches are not read. A length
- * above max_pages * page_size or an entry outside [0, n_pages) that a call
+ * above max_pages * page_size (or 2^30), or an entry outside [0, n_pages) that a call
  * needs is reported by imem_sync as IMEM_ERR_RANGE (nothing out of bounds is
  * read or written; that sequence's results are unspecified). A tok_start that
  * descends or leaves [0, n_tokens] is reported likewise, every result of the

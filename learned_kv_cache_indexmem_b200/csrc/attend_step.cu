@@ -123,7 +123,7 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     // the table entries of 32 boxes at a time, one per lane: a stage's boxes
     // then cost a shuffle instead of a load's latency
     const int boxes = (n * kRows + box - 1) / box;
-    int pids = -1;
+    int pids = -1, issued = 0;
     for (int j = 0; j < n; ++j) {
       const int first = j * parts;
       if ((first & 31) == 0) {
@@ -141,6 +141,7 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       }
       if (lane == 0) tc::mbar_expect_tx(full + 8 * st, bytes);
       __syncwarp();
+      issued = j + 1;
       if (load) {
         const int y = (pid << a.pg.page_log) + (((b0 + j) * kRows) & (page - 1) & ~(box - 1));
         const uint32_t dst = sR + st * 2 * C::tile + lane * box * 128;
@@ -151,6 +152,9 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
         }
       }
     }
+    // whatever happened, no copy is in flight when the ring is given up
+    for (int j = max(0, issued - C::stages); j < issued; ++j)
+      if (!tc::mbar_wait(full + 8 * (j % C::stages), (j / C::stages) & 1)) record_error(err, DEV_TIMEOUT);
   } else {
     // -------------------------------------------------------------- consumers
     const float sl2 = a.scale * kLog2e;

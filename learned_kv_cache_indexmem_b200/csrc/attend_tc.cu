@@ -191,7 +191,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
       auto page_of = [&](int j) {
         return needs(j) ? table[((b0 + j) * kKeys + lane * box) >> a.pg.page_log] : -1;
       };
-      int next = page_of(0);
+      int next = page_of(0), issued = 0;
       bool ok = true;
       for (int j = 0; j < n && ok; ++j) {
         const int pid = next;
@@ -209,6 +209,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
           }
           if (lane == 0) tc::mbar_expect_tx(r_full + 8 * st, bytes);
           __syncwarp();
+          issued = i + 1;
           if (load) {
             const uint32_t dst = sR + st * C::tile + lane * box * 128;
 #pragma unroll
@@ -217,6 +218,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
           }
         }
       }
+      // whatever happened, no copy is in flight when the CTA ends
+      if (!tc::mbar_wait(q_full, 0)) record_error(err, DEV_TIMEOUT);
+      for (int i = max(0, issued - C::stages); i < issued; ++i)
+        if (!tc::mbar_wait(r_full + 8 * (i % C::stages), (i / C::stages) & 1)) record_error(err, DEV_TIMEOUT);
     } else if (warp == NQ * 4 && n > 0) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t IQK = tc::idesc(tc::kFmtBF16, 128, kKeys, false, false);

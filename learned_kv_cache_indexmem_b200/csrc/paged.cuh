@@ -30,7 +30,8 @@ __device__ __forceinline__ SeqInfo seq_info(int s, int batch, int n_tokens, cons
     q.n = n_tokens / batch;
     q.tok0 = s * q.n;
   }
-  const long long cap = (long long)pg.max_pages << pg.page_log;
+  // 2^30 tokens at most: positions and rounded-up key counts stay ints
+  const long long cap = min((long long)pg.max_pages << pg.page_log, 1LL << 30);
   const int len = pg.len[s];
   q.len = (int)min((long long)max(len, 0), cap);
   q.bad |= len != q.len;

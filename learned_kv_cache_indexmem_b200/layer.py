@@ -270,9 +270,10 @@ class IndexMemLayer:
         returns the row stride."""
         d, s = self._d, x.stride()
         if x.shape == (n, heads, d) and x.dtype is self.torch_dtype and \
-                x.get_device() == self._index and s[2] == 1 and (s[1] == d or heads == 1):
+                x.get_device() == self._index and s[2] == 1 and (s[1] == d or heads == 1) and \
+                (n < 2 or s[0] >= heads * d):
             return s[0] if n > 1 else 0
-        raise ValueError("%s must be %s [%d, %d, %d] on %s, the heads of a row contiguous; got %s %s"
+        raise ValueError("%s must be %s [%d, %d, %d] on %s, rows apart and their heads contiguous; got %s %s"
                          " with strides %s on %s" % (name, self.torch_dtype, n, heads, d,
                                                      self._device, x.dtype, tuple(x.shape), s,
                                                      x.device))
@@ -358,7 +359,8 @@ class IndexMemLayer:
                      max_len: Optional[int] = None, scale: Optional[float] = None, out=None,
                      lse=None, return_lse: bool = False, stream=None):
         """Causal attention of the new tokens q [T, Hq, d] over the paged cache
-        (their own rows appended before). max_new: most new tokens of a sequence
+        (their own rows appended before), out not overlapping q. scale: of the
+        logits (default 1/sqrt(d)). max_new: most new tokens of a sequence
         (default: T, or T / b without tok_start); max_len: the longest kv_len
         expected (a hint; default: what the table can hold). Returns out, or
         (out, lse [T, Hq] fp32) with return_lse."""
@@ -374,8 +376,10 @@ class IndexMemLayer:
                 raise ValueError("lse must be contiguous float32 [%d, %d]" % (T, Hq))
         elif return_lse:
             lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+        if scale is not None and not 1e-30 < scale < 1e30:
+            raise ValueError("scale must be positive and finite")
         if max_new is None:
-            max_new = T if tok_start is not None else T // b
+            max_new = T if tok_start is not None else T // max(b, 1)
         if max_len is None:
             max_len = min(pg.max_pages * pg.page_size, 2 ** 31 - 1)
         if T:

@@ -477,6 +477,10 @@ def test_layer_refuses_tensors_that_do_not_fit(cuda_device):
                lambda: lay.rotate(bt.q, None, pos.long()),
                lambda: lay.rotate(bt.q.cpu(), None, pos),
                lambda: lay.rotate(bt.q.transpose(1, 2).contiguous().transpose(1, 2), None, pos),
+               lambda: lay.rotate(bt.q[:1].expand(8, -1, -1), None, pos),
+               lambda: lay.attend_paged(bt.q, c, scale=0.0),
+               lambda: lay.attend_paged(bt.q, c, scale=float("nan")),
+               lambda: lay.attend_paged(bt.q, c, out=bt.q[:1].expand(8, -1, -1)),
                lambda: lay.append_paged(bt.k, bt.v[:, :1], c),
                lambda: lay.append_paged(bt.k, bt.v, c, tok_start=pos),
                lambda: lay.attend_paged(bt.q, c, tok_start=bt.start.cpu()),
