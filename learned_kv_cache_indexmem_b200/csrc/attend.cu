@@ -44,7 +44,7 @@ constexpr int kThreads = 128;
 constexpr float kGrow = 8.f;             // log2 growth of a maximum that is left alone
 
 template <int D, int KS> struct F32Cfg {
-  static constexpr int keys = KS == 1 ? 32 : 64;             // per stage
+  static constexpr int keys = 32;                            // per stage
   // row strides in floats: 16-byte loads of neighbouring rows (K: rows g, V:
   // rows 2 t) then fall on different banks
   static constexpr int ks = D + 16, vs = D + 4, os = D + 4;
@@ -379,12 +379,12 @@ cudaError_t launch_f32(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
   constexpr int BM = 64 / KS, kKeys = F32Cfg<D, KS>::keys, most = KS == 1 ? 8 : 16;
   const int tiles = (a.max_new * c.group + BM - 1) / BM;
   // CTAs that have rows, about; keys are split until four of them per SM, with
-  // at least four stages each
+  // at least four stages each (one stage where the rows are few)
   const long long packed = ((long long)a.n_tokens * c.group + BM - 1) / BM;
   const int seqs = a.batch < a.n_tokens ? a.batch : a.n_tokens;
   const long long busy = (packed > seqs ? packed : seqs) * c.cfg.n_kv_heads;
   int S = 1;
-  while (S < most && busy * S < 4 * c.num_sms && (long long)a.max_len >= 2LL * S * 4 * kKeys) S *= 2;
+  while (S < most && busy * S < 4 * c.num_sms && (long long)a.max_len >= 2LL * S * (KS == 1 ? 4 : 1) * kKeys) S *= 2;
   const long long grid = (long long)tiles * a.batch * c.cfg.n_kv_heads * S;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto k = attend_f32_kernel<D, KS>;

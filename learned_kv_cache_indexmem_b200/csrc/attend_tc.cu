@@ -36,6 +36,7 @@
 #include "tc.cuh"
 
 #include <atomic>
+#include <mutex>
 #include <type_traits>
 
 namespace imem {
@@ -508,18 +509,70 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
   tc::cluster_sync_all();   // no CTA leaves while its state may still be read
 }
 
+// How many CTAs share a tile's keys, and what that is expected to take (us).
+struct Plan {
+  int S;
+  double us;
+};
+
+// Keys are split while the clusters stay one wave (16 clusters of 8 do not all
+// fit the GPU's processor groups: 47 against 26 us for eight sequences of 30
+// tokens at 7518 keys) and a CTA keeps two key tiles. A CTA takes about 7 us to
+// start and end, and per key tile 1.8 us with two query tiles, 1.3 with one.
 template <int D, int NQ>
-cudaError_t launch(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
+cudaError_t plan(const Ctx& c, const AttendArgs& a, Plan* p) {
+  using C = TcCfg<D, NQ>;
+  // once per device: attributes, and how many clusters of 1, 2, 4, 8 are resident
+  static std::atomic<const int (*)[4]> setup[64];
+  static std::mutex setup_mu;
+  const int dv = c.device & 63;
+  const int(*resident)[4] = setup[dv].load(std::memory_order_acquire);
+  if (!resident) {
+    std::lock_guard<std::mutex> lock(setup_mu);
+    resident = setup[dv].load(std::memory_order_relaxed);
+    if (!resident) {
+      auto k = attend_tc_kernel<D, NQ>;
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::total);
+      static int table[64][4];
+      cudaLaunchConfig_t cfg = {};
+      cfg.blockDim = dim3(C::threads, 1, 1);
+      cfg.dynamicSmemBytes = C::total;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      for (int s = 0; s < 4 && e == cudaSuccess; ++s) {
+        cfg.gridDim = dim3(1 << s, 1, 1);
+        attr[0].val.clusterDim.x = 1 << s;
+        e = cudaOccupancyMaxActiveClusters(&table[dv][s], k, &cfg);
+      }
+      if (e != cudaSuccess) return e;
+      resident = &table[dv];
+      setup[dv].store(resident, std::memory_order_release);
+    }
+  }
+  // tiles that have rows: about packed tokens over full tiles, one for each
+  // sequence with tokens at least
+  const long long packed = ((long long)a.n_tokens * c.group + NQ * 128 - 1) / (NQ * 128);
+  const int seqs = a.batch < a.n_tokens ? a.batch : a.n_tokens;
+  const long long busy = (packed > seqs ? packed : seqs) * c.cfg.n_kv_heads;
+  int s = 0;
+  while (s < 3 && busy <= (*resident)[s + 1] && (long long)a.max_len >= (4LL << s) * kKeys) ++s;
+  const int fit = (*resident)[s] > 0 ? (*resident)[s] : 1;
+  const double waves = (double)((busy + fit - 1) / fit);
+  const double key_tiles = (a.max_len / kKeys + 1.0) / (1 << s);
+  p->S = 1 << s;
+  p->us = waves * (7.0 + key_tiles * (NQ == 2 ? 1.8 : 1.3));
+  return cudaSuccess;
+}
+
+template <int D, int NQ>
+cudaError_t launch(const Ctx& c, const AttendArgs& a, int S, cudaStream_t st) {
   using C = TcCfg<D, NQ>;
   const int G = c.group, Hkv = c.cfg.n_kv_heads;
   const int tiles = (a.max_new * G + NQ * 128 - 1) / (NQ * 128);
-  // CTAs that have rows: about packed tokens over full tiles, one for each
-  // sequence with tokens at least
-  const long long packed = ((long long)a.n_tokens * G + NQ * 128 - 1) / (NQ * 128);
-  const int seqs = a.batch < a.n_tokens ? a.batch : a.n_tokens;
-  const long long busy = (packed > seqs ? packed : seqs) * Hkv;
-  int S = 1;
-  while (S < 8 && busy * S * 2 <= c.num_sms && (long long)a.max_len >= 4LL * S * kKeys) S *= 2;
   const long long grid = (long long)tiles * a.batch * Hkv * S;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int box = 1 << (a.pg.page_log < 7 ? a.pg.page_log : 7);
@@ -529,14 +582,6 @@ cudaError_t launch(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
       !make_tmap_bf16(c, &mk, a.pg.k, (uint64_t)Hkv * D, rows, box) ||
       !make_tmap_bf16(c, &mv, a.pg.v, (uint64_t)Hkv * D, rows, box))
     return cudaErrorInvalidValue;
-  auto k = attend_tc_kernel<D, NQ>;
-  static std::atomic<uint64_t> attr_done{0};   // one bit per device
-  const uint64_t bit = 1ull << (c.device & 63);
-  if (!(attr_done.load() & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::total);
-    if (e != cudaSuccess) return e;
-    attr_done.fetch_or(bit);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(C::threads, 1, 1);
@@ -549,13 +594,22 @@ cudaError_t launch(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, mq, mk, mv, a, c.cfg.n_q_heads, Hkv, G, S, tiles, c.err);
+  return cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, NQ>, mq, mk, mv, a, c.cfg.n_q_heads, Hkv, G, S,
+                            tiles, c.err);
 }
 
+// One or two query tiles per CTA, whichever is expected to be faster: two pass
+// over the keys at 0.9 us per tile and query tile, one fills the SMs with half
+// the rows (two sequences of 543 tokens at 1302 keys 15.4 against 20.2 us, 512
+// tokens at 131072 keys 1435 against 880).
 template <int D>
 cudaError_t launch_d(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
-  // one query tile where no sequence fills two
-  return a.max_new * c.group <= 128 ? launch<D, 1>(c, a, st) : launch<D, 2>(c, a, st);
+  Plan one, two;
+  cudaError_t e = plan<D, 1>(c, a, &one);
+  if (e == cudaSuccess) e = plan<D, 2>(c, a, &two);
+  if (e != cudaSuccess) return e;
+  return a.max_new * c.group <= 128 || one.us < two.us ? launch<D, 1>(c, a, one.S, st)
+                                                       : launch<D, 2>(c, a, two.S, st);
 }
 
 }  // namespace
