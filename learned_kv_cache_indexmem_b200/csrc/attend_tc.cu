@@ -10,14 +10,16 @@
 //   MMA warp       S_t = Q_t K^T into TMEM; O_t += P_t V with P_t from TMEM;
 //   4 warps per tile  one row per thread: S from TMEM, running maximum, exp2,
 //                  P as bf16 back into the columns of S, the row's sum.
-// While one tile's softmax runs, the tensor core works on the other tile.
-// The MMA warp's loop stays converged and one elected lane issues: its operands
-// are then uniform (a branch on the lane cost 11 %: 474 against 426 us for 2048
-// tokens at 16384 keys; a warp per query tile 562 us). MMAs of one thread run in order, so S_t of the next key tile may overwrite
+// While one tile's softmax runs, the tensor core works on the other tile. The
+// MMA warp's loop stays converged and one elected lane issues: its operands are
+// then uniform (a branch on the lane cost 11 %: 474 against 426 us for 2048
+// tokens at 16384 keys; a warp per query tile 562 us).
+//
+// MMAs of one thread run in order, so S_t of the next key tile may overwrite
 // P_t once O_t += P_t V has been issued before it, and S_t being complete
 // means that the product before it is: O_t may then be rescaled without a
-// further wait. It is rescaled only when a row's maximum has grown by more than a
-// factor of 2^8 since it was last taken: until then the sums stay below
+// further wait. It is rescaled only when a row's maximum has grown by more
+// than a factor of 2^8 since it was last taken: until then the sums stay below
 // 2^8 times what they would be, far inside fp32 and bf16.
 //
 // Keys past a row's position are masked by selection, so nothing stored there

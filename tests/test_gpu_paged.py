@@ -353,6 +353,49 @@ def test_attend_reports_bad_pages(cuda_device, dtype, new):
     lay.close()
 
 
+@pytest.mark.parametrize("dtype,d,new", [("bf16", 128, 2), ("bf16", 64, 70), ("bf16", 128, 200), ("fp32", 64, 1),
+                                         ("fp32", 128, 33)])
+def test_attend_where_nothing_or_little_is_seen(cuda_device, dtype, d, new):
+    """Sequences of length 0 (all new tokens are padding in front), of one key,
+    and two that share their pages; max_len as a wrong hint."""
+    lay = layer(cuda_device, 8, 2, d, dtype)
+    bt = batch(cuda_device, [new] * 4, [0, 1, 300, 300], 8, 2, d, dtype)
+    bt.cache.block_table[3] = bt.cache.block_table[2]
+    for hint in (None, 0, 7, 1 << 20):
+        out, lse = lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=new, max_len=hint, return_lse=True)
+        lay.sync()
+        assert (out[:new] == 0).all() and (lse[:new] == -np.inf).all()
+        check_attend(out, lse, bt, None)
+    lay.close()
+
+
+def test_chunk_attention_in_a_graph_follows_its_inputs(cuda_device):
+    """A captured chunk call replayed with other queries, pages and lengths."""
+    lay = layer(cuda_device, 8, 2, 128)
+    bt = batch(cuda_device, [90, 50], [400, 700], 8, 2, 128)
+    out, lse = torch.empty_like(bt.q), torch.empty(140, 8, device=cuda_device)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    call = lambda: lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=90, out=out, lse=lse)
+    with torch.cuda.stream(stream):
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            call()
+        other = batch(cuda_device, [40, 80], [230, 701], 8, 2, 128, seed=9)
+        small = torch.arange(other.cache.K.shape[0])
+        assert other.cache.K.shape[0] <= bt.cache.K.shape[0]
+        bt.cache.K[:len(small)], bt.cache.V[:len(small)] = other.cache.K, other.cache.V
+        bt.cache.block_table[:, :other.cache.block_table.shape[1]] = other.cache.block_table
+        bt.cache.kv_len.copy_(other.cache.kv_len), bt.start.copy_(other.start)
+        bt.q[:120] = other.q
+        graph.replay()
+    stream.synchronize()
+    lay.sync()
+    check_attend(out[:120], lse[:120], other, None)
+    lay.close()
+
+
 def test_caches_past_32_bit_offsets(cuda_device):
     """Pages whose rows lie more than 2^32 bytes and 2^31 elements into the cache."""
     hq, hkv, d, page = 8, 8, 128, 64
