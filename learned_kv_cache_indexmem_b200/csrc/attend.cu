@@ -19,11 +19,12 @@
 //
 // A tile's rows are the new tokens of one sequence times the G query heads of
 // one KV head (row r: token r / G, head r % G), so that K and V are read once
-// for the whole group. Stages of keys come by cp.async, one ahead. Each of four
-// warps has 16 rows (KS = 1), or, with at most 16 rows in all, the same rows
-// and a quarter of each stage's keys (KS = 4). The contraction's index order
-// is free: queries and keys are taken four dimensions a lane (one 16-byte load
-// for an MMA step), values four columns a lane.
+// for the whole group. Stages of 32 keys come by cp.async, one ahead. Each of
+// four warps has 16 rows (KS = 1), or, with at most 32 or 16 rows in all, two or
+// four warps share 16 rows and have a part of each stage's keys (KS = 2, 4).
+// The contraction's index order is free: queries and keys are taken four
+// dimensions a lane (one 16-byte load for two MMA steps), values four columns
+// a lane.
 //
 // The keys of a tile are split over a cluster of CTAs when there are too few
 // tiles to fill the GPU; the states (m, l, O) meet over distributed shared
@@ -51,7 +52,7 @@ template <int D, int KS> struct F32Cfg {
   static constexpr int k = keys * ks, v = keys * vs;       // floats of a buffer
   static constexpr int total = 2 * (k + v) * 4;
   static constexpr int state = 16 * os + 32;                 // a warp's (m, l, O), floats
-  static_assert((KS == 1 ? 4 : 5) * state * 4 <= total, "the states take the buffers' place");
+  static_assert((KS == 1 ? 4 : 4 + 4 / KS) * state * 4 <= total, "the states take the buffers' place");
 };
 
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool valid) {
@@ -136,7 +137,7 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
 
   // this lane's rows g and g + 8 of the warp's 16, and their queries: step 2 u
   // of the contraction takes dimensions 16 u + 4 t and + 1, step 2 u + 1 the next two
-  const int w_row = (KS == 1 ? warp * 16 : 0) + g;
+  const int w_row = warp / KS * 16 + g;
   float q[2][D / 4];
   int pos[2];
 #pragma unroll
@@ -165,7 +166,7 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
       asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     }
     __syncthreads();
-    const int w_key = KS == 1 ? 0 : (warp % KS) * 8 * NT;   // the warp's keys of the stage
+    const int w_key = warp % KS * 8 * NT;   // the warp's keys of the stage
     const float* kb = s_k + buf * C::k + (w_key + g) * C::ks + 4 * t;
     const float* vb = s_v + buf * C::v + (w_key + 2 * t) * C::vs + 4 * g;
     float s[NT][4], lo[NT][4];
@@ -340,29 +341,30 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
       x.z = x.z * fa + y.z * fb; x.w = x.w * fa + y.w * fb;
     }
   };
-  float* c_st = smem + 4 * C::state;   // KS = 4: the CTA's own state
+  float* c_st = smem + 4 * C::state;   // KS > 1: the CTA's own states, 16 rows each
   for (int i = tid; i < n_tile * (D / 4); i += kThreads) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     if (KS == 1 && S > 1) break;       // one state a row already
     float mm, ll;
     float4 x;
     meet(KS, [&](int k, float2& ml, float4& y) {
-      const float* so = smem + (KS == 1 ? r >> 4 : k) * C::state;
+      const float* so = smem + ((r >> 4) * KS + k) * C::state;
       ml = *reinterpret_cast<const float2*>(so + 16 * C::os + 2 * (r & 15));
       y = *reinterpret_cast<const float4*>(so + (r & 15) * C::os + c);
     }, mm, ll, x);
     if (S == 1) {
       finish(r, c, mm, ll, x);
     } else {
-      *reinterpret_cast<float4*>(c_st + r * C::os + c) = x;
-      if (c == 0) *reinterpret_cast<float2*>(c_st + 16 * C::os + 2 * r) = make_float2(mm, ll);
+      float* so = c_st + (r >> 4) * C::state;
+      *reinterpret_cast<float4*>(so + (r & 15) * C::os + c) = x;
+      if (c == 0) *reinterpret_cast<float2*>(so + 16 * C::os + 2 * (r & 15)) = make_float2(mm, ll);
     }
   }
   if (S == 1) return;
   tc::cluster_sync_all();
   for (int i = rank * kThreads + tid; i < n_tile * (D / 4); i += S * kThreads) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    const uint32_t so = tc::smem_addr(KS == 1 ? smem + (r >> 4) * C::state : c_st);
+    const uint32_t so = tc::smem_addr((KS == 1 ? smem : c_st) + (r >> 4) * C::state);
     float mm, ll;
     float4 x;
     meet(S, [&](int k, float2& ml, float4& y) {
@@ -376,7 +378,7 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
 
 template <int D, int KS>
 cudaError_t launch_f32(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
-  constexpr int BM = 64 / KS, kKeys = F32Cfg<D, KS>::keys, most = KS == 1 ? 8 : 16;
+  constexpr int BM = 64 / KS, kKeys = F32Cfg<D, KS>::keys, most = 16;
   const int tiles = (a.max_new * c.group + BM - 1) / BM;
   // CTAs that have rows, about; keys are split until four of them per SM, with
   // at least four stages each (one stage where the rows are few)
@@ -414,7 +416,9 @@ cudaError_t launch_f32(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_d(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
-  return a.max_new * c.group <= 16 ? launch_f32<D, 4>(c, a, st) : launch_f32<D, 1>(c, a, st);
+  const int rows = a.max_new * c.group;
+  return rows <= 16 ? launch_f32<D, 4>(c, a, st)
+                    : rows <= 32 ? launch_f32<D, 2>(c, a, st) : launch_f32<D, 1>(c, a, st);
 }
 
 }  // namespace

@@ -284,6 +284,8 @@ CASES = [
     ("fp32", 128, 8, 2, 64, [1], [5000]),
     ("fp32", 64, 8, 2, 16, [100, 1, 0, 31], [100, 400, 5, 90]),
     ("fp32", 128, 4, 4, 32, [65], [700]),
+    ("fp32", 128, 1, 1, 32, [17, 30], [5000, 31]),
+    ("fp32", 64, 8, 2, 64, [8, 5, 1], [3001, 5, 64]),
     ("fp32", 64, 8, 1, 128, [3, 9], [300, 9]),
 ]
 
