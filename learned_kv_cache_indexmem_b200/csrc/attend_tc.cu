@@ -76,7 +76,10 @@ __device__ __forceinline__ void exp2_fma(uint64_t y, float& e0, float& e1) {
   e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
   e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
-constexpr int kFmaOf8 = 1;       // of 8 neighbouring pairs, those taken by exp2_fma (0: 2 % slower, 3: 2 %)
+// Of 8 neighbouring pairs, those taken by exp2_fma: with heads of 128 one (none
+// or three: 2 % slower), with heads of 64, where the products take half the
+// time, two (none: 7 % slower, one or three: 4 %).
+template <int D> constexpr int kFmaOf8 = D == 64 ? 2 : 1;
 
 template <int D, int NQ> struct TcCfg {
   static constexpr int threads = NQ * 128 + 128;
@@ -389,7 +392,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
               tc::pack2(__uint_as_float(v[x & 31]), __uint_as_float(v[(x & 31) + 1])), scale2, nm2);
           float e0, e1;
           // masked scores are -inf: exactly 0 from the special-function unit
-          if (!decltype(masked)::value && ((x >> 1) * kFmaOf8) % 8 < kFmaOf8) {
+          if (!decltype(masked)::value && ((x >> 1) * kFmaOf8<D>) % 8 < kFmaOf8<D>) {
             exp2_fma(y, e0, e1);
           } else {
             tc::unpack2(y, e0, e1);
