@@ -15,8 +15,13 @@
 // its own: two independent tiles per warp hide the MMAs' latency (one tile of
 // 16 keys of every stage per warp: 1.3 us a stage with 20 rows), and no
 // block barrier is in the loop. 96 KB of ring, two CTAs per SM, so that one's
-// start and end hide behind the other's stream. The CTAs of a sequence and KV head form a cluster; their
-// warps' states meet over distributed shared memory at the end.
+// start and end hide behind the other's stream. The CTAs of a sequence and KV
+// head form a cluster; their warps' states meet over distributed shared memory
+// at the end.
+//
+// One token of 64 sequences of up to 32768 keys (6.5 GB): 916 us, 7.1 TB/s; of
+// one sequence of 4096 keys: 8 us; 5 tokens of four sequences of up to 16384
+// keys in pages of 16: 48 us, 4.4 TB/s (the longest sequence's CTAs last).
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"

@@ -5,7 +5,8 @@
 // Bound by HBM: K and V rows (Hkv * d elements each) are read and written
 // once. A group of lanes copies one token's K and V row; each lane has up to
 // eight 16-byte loads in flight, and the group's index and table lookups are
-// the only dependent reads before them.
+// the only dependent reads before them. 117,965 rows of 2 + 2 KB: 149 us,
+// 6.5 TB/s (the copy rate); 4 x 1024 rows: 5 us.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"

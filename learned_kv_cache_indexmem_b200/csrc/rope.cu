@@ -18,7 +18,8 @@
 // all its heads) and the cache rows, then rotate and store. A work item is 32
 // bytes of a head: two 16-byte vectors, in the half layout the two that hold
 // a pair's halves, so that every access is a full vector and no element is
-// read twice.
+// read twice. 64K tokens of 40 heads of 128: 203 us, 6.6 TB/s (the copy rate);
+// append of 26,752 tokens, 48 heads' rows each: 105 us, 6.3 TB/s.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.cuh"
