@@ -309,6 +309,8 @@ class IndexMemLayer:
         """Rotary positions: q [T, Hq, d] and k [T, Hkv, d] (either may be None)
         turned by positions [T]; returns (q_out, k_out). The outputs may be the
         inputs."""
+        if q is None and k is None:
+            raise ValueError("rotate needs q or k")
         T = (k if q is None else q).shape[0]
         self._ints("positions", positions, (T,))
         qs = qos = ks = kos = 0

@@ -518,6 +518,7 @@ def test_layer_refuses_tensors_that_do_not_fit(cuda_device):
     pos = torch.zeros(8, dtype=torch.int32, device=cuda_device)
     c = bt.cache
     for fn in (lambda: lay.rotate(bt.q.float(), None, pos),
+               lambda: lay.rotate(None, None, pos),
                lambda: lay.rotate(bt.q, bt.k[:4], pos),
                lambda: lay.rotate(bt.q, None, pos.long()),
                lambda: lay.rotate(bt.q.cpu(), None, pos),
