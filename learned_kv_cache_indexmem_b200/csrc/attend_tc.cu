@@ -28,7 +28,7 @@
 //
 // Bound by the tensor cores and exp2 for long chunks (8192 new tokens at
 // 131072, 32 heads of 128: 14.1 ms, 1.21 PFLOP/s; four ragged prompts of up to
-// 4096: 365 us, 1.04 PFLOP/s), by HBM for a few tokens.
+// 4096: 357 us, 1.06 PFLOP/s), by HBM for a few tokens.
 //
 // With too few tiles to fill the GPU the keys of a tile are split over a
 // cluster; the states (m, l, O) meet over distributed shared memory and are
@@ -129,6 +129,20 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
   const int seq = idx % a.batch;
   const int tile = tiles - 1 - idx / a.batch;
 
+  if (tid == 0) {
+    for (int i = 0; i < C::stages; ++i) {
+      tc::mbar_init(r_full + 8 * i, 1);
+      tc::mbar_init(r_empty + 8 * i, 1);
+    }
+    for (int t = 0; t < NQ; ++t) {
+      tc::mbar_init(s_full + 8 * t, 1);
+      tc::mbar_init(p_full + 16 * t, 4);
+      tc::mbar_init(p_full + 16 * t + 8, 4);
+      tc::mbar_init(o_full + 8 * t, 1);
+    }
+    tc::fence_mbar_init();
+  }
+
   const SeqInfo sq = seq_info(seq, a.batch, a.n_tokens, a.start, a.pg);
   if (tile == 0 && rank == 0 && h == 0 && tid == 0 && (sq.bad || sq.n > a.max_new))
     record_error(err, DEV_RANGE);
@@ -150,19 +164,21 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     cnt[t] = min(max((k + kKeys - 1) / kKeys - b0, 0), n);
   }
 
-  if (tid == 0) {
+  // the producer's first table entries and the queries' copy, behind the set-up
+  const int box = min(1 << a.pg.page_log, kKeys);
+  int first = -1;
+  if (warp == NQ * 4 + 1 && n > 0 && lane < kKeys / box && b0 * kKeys + lane * box < n_keys)
+    first = a.pg.table[(long long)seq * a.pg.max_pages + ((b0 * kKeys + lane * box) >> a.pg.page_log)];
+  if (warp == NQ * 4 + 1 && lane == 0) {
     tc::mbar_init(q_full, 1);
-    for (int i = 0; i < C::stages; ++i) {
-      tc::mbar_init(r_full + 8 * i, 1);
-      tc::mbar_init(r_empty + 8 * i, 1);
-    }
-    for (int t = 0; t < NQ; ++t) {
-      tc::mbar_init(s_full + 8 * t, 1);
-      tc::mbar_init(p_full + 16 * t, 4);
-      tc::mbar_init(p_full + 16 * t + 8, 4);
-      tc::mbar_init(o_full + 8 * t, 1);
-    }
     tc::fence_mbar_init();
+    if (n > 0) {
+      tc::mbar_expect_tx(q_full, NQ * C::tile);
+      for (int t = 0; t < NQ; ++t)
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_3d(sQ + t * C::tile + c * C::half, &mq, q_full, 64 * c, h * G,
+                          sq.tok0 + (r0 + t * 128) / G);
+    }
   }
   if (warp == NQ * 4) {
     tc::tmem_alloc(tc::smem_addr(&s_tmem), C::tmem_cols);
@@ -183,22 +199,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     if (warp == NQ * 4 + 1 && n > 0) {
       // ------------------------------------------------------------ producer
       const int page = 1 << a.pg.page_log;
-      const int box = min(page, kKeys), parts = kKeys / box;   // boxes per tile
+      const int parts = kKeys / box;   // boxes per tile
       const int32_t* table = a.pg.table + (long long)seq * a.pg.max_pages;
-      if (lane == 0) {
-        tc::mbar_expect_tx(q_full, NQ * C::tile);
-        for (int t = 0; t < NQ; ++t)
-          for (int c = 0; c < D / 64; ++c)
-            tc::tma_load_3d(sQ + t * C::tile + c * C::half, &mq, q_full, 64 * c, h * G,
-                            sq.tok0 + (r0 + t * 128) / G);
-      }
       auto needs = [&](int j) {   // this lane has a box of key tile j
         return j < n && lane < parts && (b0 + j) * kKeys + lane * box < n_keys;
       };
       auto page_of = [&](int j) {
         return needs(j) ? table[((b0 + j) * kKeys + lane * box) >> a.pg.page_log] : -1;
       };
-      int next = page_of(0), issued = 0;
+      int next = first, issued = 0;
       bool ok = true;
       for (int j = 0; j < n && ok; ++j) {
         const int pid = next;
@@ -437,6 +446,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
   const bool mine = n > 0 && cnt[my] > 0;
   if (S == 1) {
     const float inv = l != 0.f ? 1.f / l : 0.f;
+    // whole 32-byte sectors where the rows allow it
+    const bool wide = (((uintptr_t)a.out | (uintptr_t)(a.out_stride * 2)) & 31) == 0;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -450,11 +461,22 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
       if (row < n_rows) {
         __nv_bfloat16* p = out_at(row) + 32 * c;
 #pragma unroll
-        for (int x = 0; x < 32; x += 8) {
-          float f[8];
+        for (int x = 0; x < 32; x += 16) {
+          uint32_t y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[x + e]) * inv;
-          store8(p + x, f);
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[x + 2 * e]) * inv,
+                                                           __uint_as_float(o[x + 2 * e + 1]) * inv);
+            y[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p + x), "r"(y[0]),
+                         "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                         : "memory");
+          } else {
+            *reinterpret_cast<uint4*>(p + x) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(p + x + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
         }
       }
     }

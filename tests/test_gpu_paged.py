@@ -312,6 +312,15 @@ def test_attend(cuda_device, dtype, d, hq, hkv, page, news, lens):
     lay.sync()
     check_attend(view, None, bt, None, scale=0.3)
     assert (wide[:, 0] == 0).all() and (wide[:, 1 + hq:] == 0).all()
+    # an output that is aligned to 16 bytes and no more
+    step = 16 // bt.q.element_size()
+    odd = torch.zeros(bt.q.numel() + 2 * step, dtype=bt.q.dtype, device=cuda_device)
+    view = odd[step:-step].view(bt.q.shape)
+    assert view.data_ptr() % 32 == 16
+    lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=max(news), out=view)
+    lay.sync()
+    check_attend(view, None, bt, None)
+    assert (odd[:step] == 0).all() and (odd[-step:] == 0).all()
     lay.close()
 
 
