@@ -5,6 +5,7 @@ Plumbing only -- every step of the path runs in libindexmem.so's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Optional
 
@@ -238,6 +239,19 @@ class IndexMemLayer:
                          st.K_ret.shape[1], st.M, st.bstab, out, on.evicted, self._ws, stream)
         return out
 
+    def _as_current(self, stream):
+        """Makes ``stream`` (a torch stream or a handle; None: the current one)
+        torch's current stream, so that what is allocated and filled inside
+        belongs to it."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = int(getattr(stream, "cuda_stream", stream))
+            # an ExternalStream of handle 0 would be a new stream of torch's pool
+            stream = (torch.cuda.ExternalStream(handle, device=self._device) if handle
+                      else torch.cuda.default_stream(self._device))
+        return torch.cuda.stream(stream)
+
     # -- rotary positions and the paged cache -----------------------------------
     def set_rope(self, rot_dim: Optional[int] = None, base: float = 10000.0, layout: str = "half",
                  scaling: str = "plain", factor: float = 1.0, low: float = 1.0, high: float = 4.0,
@@ -425,10 +439,17 @@ class IndexMemLayer:
         reported by sync as IMEM_ERR_RANGE); the pages are free to be reused
         once the stream has passed this call."""
         b, L = X.shape[0], X.shape[1]
-        at = torch.arange(L, dtype=torch.int32, device=X.device).expand(b, L).contiguous()
-        K, V = self.gather_paged(cache, at, stream=stream)
-        self.score_and_evict(X, Q, K, V, st, B, stream=stream)
-        self.update_memory(K, V, st, B, chunk=chunk, stream=stream)
+        caller = torch.cuda.current_stream(self._device)
+        # positions, rows and a new workspace are made on the call's stream: filled
+        # in its order, and their memory not given out again before it is through
+        with self._as_current(stream):
+            at = torch.arange(L, dtype=torch.int32, device=X.device).expand(b, L).contiguous()
+            K, V = self.gather_paged(cache, at)
+            self.score_and_evict(X, Q, K, V, st, B)
+            self.update_memory(K, V, st, B, chunk=chunk)
+            # the workspace stays with the layer, for calls on either stream
+            self._ws.record_stream(torch.cuda.current_stream(self._device))
+            self._ws.record_stream(caller)
 
     def sync(self, stream=None):
         B_.sync(self.ctx, stream)

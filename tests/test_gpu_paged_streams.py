@@ -1,0 +1,91 @@
+"""The paged calls on a stream that is not torch's current one: what they make
+for themselves is ordered with the call's stream, whatever the current stream
+does before or after."""
+import numpy as np
+import pytest
+import torch
+
+from learned_kv_cache_indexmem_b200 import synth
+from learned_kv_cache_indexmem_b200.layer import IndexMemLayer
+
+pytestmark = pytest.mark.gpu
+LONG = 100_000_000     # cycles of a kernel that only waits: some 50 ms
+
+
+def _prompt(dev, L=320, page=16):
+    """A layer, a prompt of two sequences in pages, its hidden states and queries."""
+    wl = synth.WORKLOADS["c0"]
+    w = synth.make_weights(wl.shape, 5, dev)
+    x = synth.make_layer_inputs(wl, w, 5, dev, L=L, batch=2)
+    lay = IndexMemLayer.from_shape(wl.shape, w)
+    lay.set_rope()
+    pages = lay.new_paged(2, 2 * L // page, page, L // page, dev)
+    pages.block_table.copy_(torch.from_numpy(np.random.default_rng(0).permutation(2 * L // page)).view(2, -1))
+    pages.kv_len.fill_(L)
+    lay.append_paged(x["K"].flatten(0, 1), x["V"].flatten(0, 1), pages)
+    lay.sync()
+    return lay, pages, x
+
+
+def _states(st):
+    return [t.clone() for t in (st.running_max, st.idx_retained, st.idx_evicted, st.K_ret, st.V_ret, st.M, st.bstab)]
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("busy", ["current", "own"])
+def test_evict_paged_on_another_stream(cuda_device, busy, handle):
+    """busy = current: work queued on the current stream before the call must not
+    delay what the call reads; busy = own: memory that the current stream takes
+    and writes after the call must not be the call's."""
+    L, Bg = 320, 48
+    lay, pages, x = _prompt(cuda_device, L)
+    st = lay.new_state(2, L, Bg, Bg, cuda_device)
+    lay.evict_paged(x["X"], x["Q"], pages, st, Bg, chunk=64)
+    lay.sync()
+    want = _states(st)
+    lay.close()
+    lay, pages, x = _prompt(cuda_device, L)
+    st = lay.new_state(2, L, Bg, Bg, cuda_device)
+    side = torch.cuda.Stream()
+    for _ in range(2):       # with a new workspace, then with the layer's own
+        st.M.zero_(), st.bstab.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        if busy == "current":
+            # blocks of every size the call needs, freed with writes still to come
+            junk = [torch.empty(1 << k, dtype=torch.uint8, device=cuda_device) for k in range(9, 23)]
+            torch.cuda._sleep(LONG)
+            for t in junk:
+                t.fill_(0x7f)
+            del junk, t
+        else:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(LONG)
+        lay.evict_paged(x["X"], x["Q"], pages, st, Bg, chunk=64, stream=side.cuda_stream if handle else side)
+        junk = [torch.full((1 << k,), 0x7f, dtype=torch.uint8, device=cuda_device) for k in range(9, 23) for _ in range(4)]
+        torch.cuda.current_stream().synchronize()
+        lay.sync(side)
+        for got, ref in zip(_states(st), want):
+            assert torch.equal(got, ref)
+        del junk
+    lay.close()
+
+
+def test_evict_paged_on_the_default_stream_from_another(cuda_device):
+    """Handle 0 is the default stream."""
+    L, Bg = 320, 48
+    lay, pages, x = _prompt(cuda_device, L)
+    st = lay.new_state(2, L, Bg, Bg, cuda_device)
+    lay.evict_paged(x["X"], x["Q"], pages, st, Bg, chunk=64)
+    lay.sync()
+    want = _states(st)
+    st.M.zero_(), st.bstab.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda._sleep(LONG)
+        assert lay._as_current(0).stream == torch.cuda.default_stream()
+        lay.evict_paged(x["X"], x["Q"], pages, st, Bg, chunk=64, stream=0)
+    lay.sync(0)
+    torch.cuda.synchronize()
+    for got, ref in zip(_states(st), want):
+        assert torch.equal(got, ref)
+    lay.close()
