@@ -89,3 +89,46 @@ def test_evict_paged_on_the_default_stream_from_another(cuda_device):
     for got, ref in zip(_states(st), want):
         assert torch.equal(got, ref)
     lay.close()
+
+
+def test_outputs_belong_to_the_stream_of_the_call(cuda_device):
+    """rotate, append, attend and gather on another stream, their outputs left to
+    them: blocks that the current stream has freed, but has yet to write, are not
+    taken for them; what the current stream takes afterwards is not theirs."""
+    lay, pages, x = _prompt(cuda_device)
+    q, k, v = (x[n].flatten(0, 1) for n in ("Q", "K", "V"))
+    pos = torch.arange(q.shape[0], dtype=torch.int32, device=cuda_device)
+
+    def calls(**kw):
+        return (lay.rotate(q, k, pos, **kw) + (lay.append_paged(k, v, pages, q=q, **kw),)
+                + lay.attend_paged(q, pages, return_lse=True, **kw) + lay.gather_paged(pages, n=300, **kw))
+
+    want = [t.clone() for t in calls()]
+    sizes = sorted({t.nbytes for t in want})
+    for handle in (False, True):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        junk = [torch.empty(n, dtype=torch.uint8, device=cuda_device) for n in sizes for _ in range(len(want))]
+        torch.cuda._sleep(LONG)
+        for t in junk:
+            t.fill_(0x7f)
+        del junk, t
+        got = calls(stream=side.cuda_stream if handle else side)
+        torch.cuda.current_stream().synchronize()
+        lay.sync(side)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        # dropped while the current stream still reads them: not given out again on theirs
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(LONG)
+        copies = [t.clone() for t in got]
+        del got, a
+        over = calls(stream=side)
+        for t in over:
+            with torch.cuda.stream(side):
+                t.fill_(1)
+        torch.cuda.synchronize()
+        for a, b in zip(copies, want):
+            assert torch.equal(a, b)
+        del over, copies
+    lay.close()
