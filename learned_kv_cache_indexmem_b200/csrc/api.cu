@@ -943,7 +943,7 @@ imem_status imem_attend_paged(imem_ctx* h, int batch, int n_tokens, const int32_
   a.batch = batch;
   a.n_tokens = n_tokens;
   a.max_new = max_new;
-  a.max_len = max_len;
+  a.max_len = max_len < (1 << 30) ? max_len : 1 << 30;   // no longer sequence exists (seq_info)
   a.start = tok_start;
   a.q = q; a.q_stride = q_stride;
   a.out = out; a.out_stride = out_stride;

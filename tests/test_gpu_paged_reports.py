@@ -1,0 +1,36 @@
+"""What the paged calls report, through the layer: lengths and token ranges that
+do not fit, a max_new that is too small, hints of any size."""
+import pytest
+import torch
+
+from learned_kv_cache_indexmem_b200 import binding as B
+
+from .test_gpu_paged import batch, check_attend, layer
+
+pytestmark = pytest.mark.gpu
+
+
+def reported(lay):
+    """The error that sync raises (none: None); the context is clean afterwards."""
+    try:
+        lay.sync()
+    except B.IndexMemError as e:
+        lay.sync()
+        return e.name
+    return None
+
+
+@pytest.mark.parametrize("dtype,new", [("bf16", 1), ("bf16", 40), ("fp32", 1)])
+def test_attend_hints_above_the_longest_length(cuda_device, dtype, new):
+    """Hints past the longest length a sequence may have (2^30) split the work as
+    that length does: the same sums in the same order."""
+    lay = layer(cuda_device, dtype=dtype)
+    bt = batch(cuda_device, [new], [3000], dtype=dtype)
+    call = lambda hint: lay.attend_paged(bt.q, bt.cache, max_len=hint, return_lse=True)
+    out, lse = call(1 << 30)
+    for hint in ((1 << 30) + 1, (1 << 31) - 64, (1 << 31) - 1):
+        o, l = call(hint)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    assert reported(lay) is None
+    check_attend(out, lse, bt, None)
+    lay.close()
