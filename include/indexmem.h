@@ -541,9 +541,11 @@ imem_status imem_append_paged(imem_ctx* ctx, int batch, int n_tokens, const int3
  *   s_j = scale q . k_j, out = sum_{j <= p} softmax(s)_j v_j     (out model dtype)
  *   lse = ln sum_{j <= p} exp(s_j)            (fp32 [n_tokens, Hq], or NULL)
  * A token that sees no key (p < 0) gets out = 0 and lse = -inf. Keys and values
- * past kv_len are never used, whatever the pages hold there. Within a chunk a
- * value row that is not finite may also reach the outputs of the 255 tokens
- * before it (0 * inf in a masked place of their tile). softmax in fp32; bf16:
+ * past kv_len are never used, whatever the pages hold there. A score of -inf has
+ * weight 0 (where a row has no other: out = 0, lse = -inf); a NaN or +inf among
+ * a row's scores makes its out NaN, its lse NaN or, with +inf, +inf. Within a
+ * chunk a value row that is not finite may also reach the outputs of the 255
+ * tokens before it (0 * inf in a masked place of their tile). softmax in fp32; bf16:
  * probabilities are rounded to bf16 for the product with V, as imem_decode
  * does; fp32: products from two tf32 halves, about fp32's own accuracy. out
  * must not overlap q or the cache.

@@ -46,11 +46,10 @@ namespace imem {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKeys = 128;       // keys per tile
 constexpr float kGrow = 8.f;     // log2 growth of a maximum that is left alone
 
-// 2^y for two values y >= -126 (below: 2^-126) on the FMA units: y = n + f with
+// 2^y for two values y >= -126 (below, and for NaN: 2^-126) on the FMA units: y = n + f with
 // n the nearest integer (added and taken off 1.5 * 2^23), 2^f on [-1/2, 1/2]
 // by the polynomial of degree 5 with the smallest largest relative error
 // (fitted by the exchange algorithm; 2.4e-7 in fp32, ex2.approx has 1.2e-7), n
@@ -363,14 +362,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
       float mx[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+        mx[c] = tc::max_nan(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
         for (int x = 2; x < 32; x += 2)
-          mx[c] = tc::max3f(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
+          mx[c] = tc::max3_nan(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
       }
-      const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      // NaN when both are -inf: not grown
-      const bool grown = m == -INFINITY ? mj > m : (mj - m) * sl2 > kGrow;
+      const float mj = tc::max_nan(tc::max_nan(mx[0], mx[1]), tc::max_nan(mx[2], mx[3]));
+      // a NaN score makes mj NaN and counts as grown: the sum and O are NaN from
+      // there on, by the factor f and by the special-function unit's columns
+      const bool grown = m == -INFINITY ? !(mj <= m) : !((mj - m) * sl2 <= kGrow);
       float f = 1.f;
       if (grown) {
         f = tc::ex2((m - mj) * sl2);
@@ -430,6 +430,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     float lo, hi;
     tc::unpack2(sum, lo, hi);
     l = lo + hi;
+    // what exp2_fma made of scores beside +inf, or of -inf alone, is no sum
+    if (m == INFINITY) l = NAN;
+    if (m == -INFINITY && l == l) l = 0.f;
     if (cnt[my] > 0 && ok && !tc::mbar_wait(o_full + 8 * my, 0)) record_error(err, DEV_TIMEOUT);
     tc::fence_after();
   }
@@ -440,8 +443,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
   };
   auto put_lse = [&](int r, float m2, float ll) {   // m2: maximum of the log2 scores
     if (a.lse)
-      a.lse[(long long)(sq.tok0 + r / G) * Hq + h * G + r % G] =
-          ll != 0.f ? (m2 + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
+      a.lse[(long long)(sq.tok0 + r / G) * Hq + h * G + r % G] = lse_of(m2, ll);
   };
   const bool mine = n > 0 && cnt[my] > 0;
   if (S == 1) {

@@ -46,4 +46,12 @@ __device__ __forceinline__ long long cache_row(const PagedView& pg, const int32_
   return ((long long)page << pg.page_log) + (pos & ((1 << pg.page_log) - 1));
 }
 
+// ln of the sum of exponentials from a row's maximum in log2 units and its sum
+// relative to that. +inf, a score of the row, is the result; a NaN stays one; a
+// sum of 0 (nothing seen, or scores of -inf alone) gives -inf.
+__device__ __forceinline__ float lse_of(float m2, float sum) {
+  if (m2 == INFINITY) return m2;
+  return sum != 0.f ? (m2 + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
 }  // namespace imem

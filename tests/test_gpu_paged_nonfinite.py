@@ -1,0 +1,108 @@
+"""NaN and infinities among the cached keys and values, through the layer's
+attend_paged, against the definition in 64 bits.
+
+By the formulas, with IEEE arithmetic for the scores s_j of the keys that a row
+sees: a score of -inf has weight 0; a NaN score makes the row's out and lse
+NaN; a score of +inf makes its out NaN and its lse +inf; a row all of whose
+scores are -inf is as one that sees nothing (out 0, lse -inf). Rows
+that see none of them keep their values within the tolerances of
+test_gpu_paged.py, which is where those are derived.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as po
+
+from .parity import to_np
+from .test_gpu_paged import U, batch, layer
+
+pytestmark = pytest.mark.gpu
+
+
+def definition(bt):
+    """out, lse, and sum_j p_j |v_j| and the largest scale sum_d |q_d k_jd| of each
+    row (over the finite entries), as po.attend, for any values."""
+    q, K, V = to_np(bt.q), to_np(bt.cache.K), to_np(bt.cache.V)
+    T, hq, d = q.shape
+    page, hkv = K.shape[1:3]
+    G, scale = hq // hkv, d ** -0.5
+    table, start = bt.cache.block_table.cpu().numpy(), bt.start.cpu().numpy()
+    out, lse = np.zeros((T, hq, d)), np.zeros((T, hq))
+    spread, size = np.zeros((T, hq, d)), np.zeros((T, hq))
+    finite = lambda x: np.where(np.isfinite(x), x, 0.0)
+    with np.errstate(invalid="ignore", over="ignore"):
+        for s, n in enumerate(bt.lens):
+            rows = po.slots(table[s], page, n)
+            k, v = K.reshape(-1, hkv, d)[rows], V.reshape(-1, hkv, d)[rows]
+            for t in range(start[s], start[s + 1]):
+                seen = n - (start[s + 1] - t) + 1
+                for h in range(hq):
+                    kk, vv = k[:seen, h // G], v[:seen, h // G]
+                    x = scale * (kk * q[t, h]).sum(1)
+                    size[t, h] = scale * (np.abs(finite(kk)) @ np.abs(q[t, h])).max()
+                    if np.isnan(x).any() or (x == np.inf).any():
+                        out[t, h] = np.nan
+                        lse[t, h] = np.nan if np.isnan(x).any() else np.inf
+                        continue
+                    if (x == -np.inf).all():
+                        out[t, h], lse[t, h] = 0.0, -np.inf
+                        continue
+                    p = np.exp(x - x.max())
+                    lse[t, h] = x.max() + np.log(p.sum())
+                    p /= p.sum()
+                    on = p > 0
+                    out[t, h] = (p[on, None] * vv[on]).sum(0)
+                    spread[t, h] = p @ np.abs(finite(vv))
+    return out, lse, spread, size
+
+
+def check(out, lse, bt):
+    ref, rl, spread, size = definition(bt)
+    o, l = to_np(out), to_np(lse)
+    d, n, e = o.shape[2], max(bt.lens), torch.finfo(out.dtype).eps / 2
+    ds = 4 * U * (d + 4) * size
+    rel = 2 * ds + 16 * U + 4 * U * (n + 4) + (e if out.dtype == torch.bfloat16 else 0.0)
+    assert np.array_equal(np.isnan(o), np.isnan(ref)), "NaN in %d outputs, by definition %d" % (
+        np.isnan(o).sum(), np.isnan(ref).sum())
+    inf = np.isinf(ref)
+    assert np.array_equal(o[inf], ref[inf]) and np.isfinite(o[~inf & ~np.isnan(ref)]).all()
+    on = np.isfinite(ref)
+    tol = rel[..., None] * spread + e * np.abs(ref)
+    assert (np.abs(o[on] - ref[on]) <= tol[on]).all()
+    on = np.isfinite(rl)
+    assert np.array_equal(np.isnan(l), np.isnan(rl)) and np.array_equal(l[np.isinf(rl)], rl[np.isinf(rl)])
+    tl = ds + 4 * U * (n + 4) + 16 * U + 4 * U * np.abs(rl)
+    assert (np.abs(l[on] - rl[on]) <= tl[on]).all()
+
+
+@pytest.mark.parametrize("kind", ["nan", "one", "inf", "all", "value"])
+@pytest.mark.parametrize("dtype,d,new", [
+    ("bf16", 64, 70), ("bf16", 64, 40), ("bf16", 128, 70), ("bf16", 128, 40),     # chunks: two tiles of rows, one
+])
+def test_non_finite_keys_and_values(cuda_device, dtype, d, new, kind):
+    """Sixteen sequences, each with one such key (or value) at another of 16
+    neighbouring positions, long before the new tokens, so that no place of its
+    tile is masked; one KV head of two."""
+    lay = layer(cuda_device, 8, 2, d, dtype)
+    lens = [640 + 3 * s for s in range(16)]
+    bt = batch(cuda_device, [new] * 16, lens, 8, 2, d, dtype, seed=d + new)
+    Kf, Vf = bt.cache.K.view(-1, 2, d), bt.cache.V.view(-1, 2, d)
+    for s in range(16):
+        rows = po.slots(bt.cache.block_table[s].tolist(), 16, lens[s])
+        at = int(rows[256 + s])
+        if kind == "nan":
+            Kf[at, 0] = float("nan")
+        elif kind == "one":
+            Kf[at, 0, d - 3] = float("nan")
+        elif kind == "inf":          # +inf or -inf by the sign of q's first element
+            Kf[at, 0, 0] = float("inf")
+        elif kind == "all":
+            Kf[torch.from_numpy(rows).to(cuda_device), 0, 0] = float("-inf")
+        else:
+            Vf[at, 0, 5], Vf[at, 0, 6], Vf[at, 0, 7] = float("inf"), float("-inf"), float("nan")
+    for hint in (None, 0):           # keys split over CTAs, and not
+        out, lse = lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=new, max_len=hint, return_lse=True)
+        lay.sync()
+        check(out, lse, bt)
+    lay.close()
