@@ -34,7 +34,6 @@ namespace imem {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 64;                // keys per stage
 constexpr int kWarps = 4;                // consumers
 constexpr int kThreads = kWarps * 32 + 32;
@@ -372,8 +371,7 @@ attend_step_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     const __nv_bfloat162 y1 = __floats2bfloat162_rn(x2 * inv, x3 * inv);
     *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + tok * a.out_stride + head * D + c) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
-    if (c == 0 && a.lse)
-      a.lse[tok * Hq + head] = ll != 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
+    if (c == 0 && a.lse) a.lse[tok * Hq + head] = lse_of(mm, ll);
   };
   // the CTA's state: its warps' meet here
   const int items = n_rows * (D / 4);

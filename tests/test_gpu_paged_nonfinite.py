@@ -79,6 +79,7 @@ def check(out, lse, bt):
 @pytest.mark.parametrize("kind", ["nan", "one", "inf", "all", "value"])
 @pytest.mark.parametrize("dtype,d,new", [
     ("bf16", 64, 70), ("bf16", 64, 40), ("bf16", 128, 70), ("bf16", 128, 40),     # chunks: two tiles of rows, one
+    ("bf16", 64, 1), ("bf16", 128, 3), ("bf16", 128, 6),                          # steps: one to three column tiles
 ])
 def test_non_finite_keys_and_values(cuda_device, dtype, d, new, kind):
     """Sixteen sequences, each with one such key (or value) at another of 16
