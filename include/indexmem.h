@@ -543,8 +543,8 @@ imem_status imem_append_paged(imem_ctx* ctx, int batch, int n_tokens, const int3
  * A token that sees no key (p < 0) gets out = 0 and lse = -inf. Keys and values
  * past kv_len are never used, whatever the pages hold there. A score of -inf has
  * weight 0 (where a row has no other: out = 0, lse = -inf); a NaN or +inf among
- * a row's scores makes its out NaN, its lse NaN or, with +inf, +inf. Within a
- * chunk a value row that is not finite may also reach the outputs of the 255
+ * a row's scores makes its out NaN, its lse NaN or, with +inf, +inf. bf16: within
+ * a chunk a value row that is not finite may also reach the outputs of the 255
  * tokens before it (0 * inf in a masked place of their tile). softmax in fp32; bf16:
  * probabilities are rounded to bf16 for the product with V, as imem_decode
  * does; fp32: products from two tf32 halves, about fp32's own accuracy. out

@@ -17,6 +17,12 @@
 // memory feeds those (1024 new tokens, 8 heads of 64: 44 us, 25 TFLOP/s; on
 // the fp32 units 56 us).
 //
+// An infinite value has no such halves (lo = inf - inf): its products are NaN
+// whatever they should be. A CTA that finds a NaN among its rows' sums and
+// outputs therefore takes its keys a second time by whole products on the fp32
+// units, where masked places do not enter at all: infinities then count as they
+// are, and what stays NaN is NaN by the formulas.
+//
 // A tile's rows are the new tokens of one sequence times the G query heads of
 // one KV head (row r: token r / G, head r % G), so that K and V are read once
 // for the whole group. Stages of 32 keys come by cp.async, one ahead. Each of
@@ -40,7 +46,6 @@ namespace imem {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 128;
 constexpr float kGrow = 8.f;             // log2 growth of a maximum that is left alone
 
@@ -53,6 +58,7 @@ template <int D, int KS> struct F32Cfg {
   static constexpr int total = 2 * (k + v) * 4;
   static constexpr int state = 16 * os + 32;                 // a warp's (m, l, O), floats
   static_assert((KS == 1 ? 4 : 4 + 4 / KS) * state * 4 <= total, "the states take the buffers' place");
+  static_assert((4 * state + 2 * keys * os) * 4 <= total, "states and a stage of whole_states");
 };
 
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool valid) {
@@ -70,6 +76,67 @@ __device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint
       "{%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The states of the CTA's rows by whole products, each warp's in its place (see
+// the kernel's end). Rare, so plain: a row at a time, a key a lane; out of line,
+// so that the kernel's own pass keeps its registers.
+template <int D, int KS>
+__device__ __noinline__ void whole_states(const AttendArgs& a, float* smem, const int32_t* table,
+                                          int h, int Hkv, int G, int r0, int n_rows, int tok0,
+                                          int past, int n_keys, int b0, int b1) {
+  using C = F32Cfg<D, KS>;
+  constexpr int kKeys = C::keys, NK = kKeys / KS;   // keys of a stage, of a warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* so = smem + warp * C::state;               // O rows, then (m in log2 units, l)
+  float* s_k = smem + 4 * C::state;
+  float* s_v = s_k + kKeys * C::os;
+  const int w_key = warp % KS * NK;
+  const float sl2 = a.scale * kLog2e;
+  __syncthreads();
+  for (int i = lane; i < 16 * C::os; i += 32) so[i] = 0.f;
+  so[16 * C::os + lane] = lane & 1 ? 0.f : -INFINITY;
+  for (int b = b0; b < b1; ++b) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kKeys * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4, key = b * kKeys + r;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      const long long row = key < n_keys ? cache_row(a.pg, table, key) : -1;
+      if (row >= 0) {
+        x = *reinterpret_cast<const float4*>((const float*)a.pg.k + (row * Hkv + h) * D + c);
+        y = *reinterpret_cast<const float4*>((const float*)a.pg.v + (row * Hkv + h) * D + c);
+      }
+      *reinterpret_cast<float4*>(s_k + r * C::os + c) = x;
+      *reinterpret_cast<float4*>(s_v + r * C::os + c) = y;
+    }
+    __syncthreads();
+    for (int r = 0; r < 16; ++r) {
+      const int row = min(r0 + warp / KS * 16 + r, n_rows - 1);
+      const int seen = past + row / G - (b * kKeys + w_key);   // the warp's last key that the row sees
+      const float* q = (const float*)a.q + (long long)(tok0 + row / G) * a.q_stride + (h * G + row % G) * D;
+      const float* k = s_k + (w_key + lane % NK) * C::os;
+      float x = 0.f;
+      for (int c = 0; c < D; c += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(q + c);
+        const float4 v = *reinterpret_cast<const float4*>(k + c);
+        x += u.x * v.x; x += u.y * v.y; x += u.z * v.z; x += u.w * v.w;
+      }
+      const bool on = lane < NK && lane <= seen;
+      x = on ? x * sl2 : -INFINITY;
+      const float2 ml = *reinterpret_cast<const float2*>(so + 16 * C::os + 2 * r);
+      const float m = fmaxf(ml.x, warp_max(x)), base = m == -INFINITY ? 0.f : m;
+      const float f = tc::ex2(ml.x - base), p = tc::ex2(x - base);
+      const float l = ml.y * f + warp_sum(on ? p : 0.f);
+      for (int d = lane; d < D; d += 32) so[r * C::os + d] *= f;
+      for (int i = 0; i < NK && i <= seen; ++i) {
+        const float pi = __shfl_sync(0xffffffffu, p, i);
+        for (int d = lane; d < D; d += 32) so[r * C::os + d] += pi * s_v[(w_key + i) * C::os + d];
+      }
+      __syncwarp();
+      if (lane == 0) *reinterpret_cast<float2*>(so + 16 * C::os + 2 * r) = make_float2(m, l);
+      __syncwarp();
+    }
+  }
 }
 
 template <int D, int KS>
@@ -297,9 +364,18 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
   }
 
+  bool odd = l[0] != l[0] || l[1] != l[1];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) odd |= o[i][e] != o[i][e];
+  odd = __syncthreads_or(odd);
+  if (odd) whole_states<D, KS>(a, smem, table, h, Hkv, G, r0, n_rows, sq.tok0, past, n_keys, b0, b1);
+
   // states: one of 16 rows for each warp, in the buffers' place
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
+    if (odd) break;
     float* so = smem + warp * C::state;
     const int r = g + 8 * e;
     if (t == 0) {
@@ -321,8 +397,7 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
     const float inv = ll != 0.f ? 1.f / ll : 0.f;
     *reinterpret_cast<float4*>((float*)a.out + tok * a.out_stride + head * D + c) =
         make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    if (c == 0 && a.lse)
-      a.lse[tok * Hq + head] = ll != 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;   // NaN stays NaN
+    if (c == 0 && a.lse) a.lse[tok * Hq + head] = lse_of(mm, ll);
   };
   // sums N states of one row, `at` giving (m, l) and four columns of the k-th
   auto meet = [&](int N, auto at, float& mm, float& ll, float4& x) {

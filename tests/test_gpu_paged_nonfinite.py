@@ -80,6 +80,7 @@ def check(out, lse, bt):
 @pytest.mark.parametrize("dtype,d,new", [
     ("bf16", 64, 70), ("bf16", 64, 40), ("bf16", 128, 70), ("bf16", 128, 40),     # chunks: two tiles of rows, one
     ("bf16", 64, 1), ("bf16", 128, 3), ("bf16", 128, 6),                          # steps: one to three column tiles
+    ("fp32", 64, 40), ("fp32", 128, 40), ("fp32", 64, 8), ("fp32", 128, 2),       # one, two, four warps to 16 rows
 ])
 def test_non_finite_keys_and_values(cuda_device, dtype, d, new, kind):
     """Sixteen sequences, each with one such key (or value) at another of 16
@@ -106,4 +107,20 @@ def test_non_finite_keys_and_values(cuda_device, dtype, d, new, kind):
         out, lse = lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=new, max_len=hint, return_lse=True)
         lay.sync()
         check(out, lse, bt)
+    lay.close()
+
+
+@pytest.mark.parametrize("d,new", [(64, 40), (128, 8), (64, 3)])
+def test_fp32_values_of_later_tokens_stay_out(cuda_device, d, new):
+    """fp32: a new token's key and value that are not finite reach that token and
+    those after it, and none before."""
+    lay = layer(cuda_device, 8, 2, d, "fp32")
+    bt = batch(cuda_device, [new, new], [300, 77], 8, 2, d, "fp32")
+    for s in range(2):
+        at = int(po.slots(bt.cache.block_table[s].tolist(), 16, bt.lens[s])[-1 - new // 2])
+        bt.cache.K.view(-1, 2, d)[at, s] = float("inf")
+        bt.cache.V.view(-1, 2, d)[at, s] = float("nan")
+    out, lse = lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=new, return_lse=True)
+    lay.sync()
+    check(out, lse, bt)
     lay.close()
