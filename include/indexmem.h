@@ -489,7 +489,7 @@ typedef enum { IMEM_ROPE_HALF = 0, IMEM_ROPE_INTERLEAVED = 1 } imem_rope_layout;
  *           / (2 pi) turns over the original context: pairs of fewer than `low`
  *           turns are stretched, of more than `high` kept
  *   RAMP    w = 1 - clamp((i - a) / max(b - a, 0.001), 0, 1) over the pair's index,
- *           a = floor(x(high)), b = ceil(x(low)), both held in [0, rot_dim/2 - 1],
+ *           a = floor(x(high)), b = ceil(x(low)), both held in [0, rot_dim - 1],
  *           x(n) = rot_dim ln(orig_len / (2 pi n)) / (2 ln base) (YaRN's ramp) */
 typedef enum { IMEM_ROPE_PLAIN = 0, IMEM_ROPE_LINEAR = 1, IMEM_ROPE_BAND = 2,
                IMEM_ROPE_RAMP = 3 } imem_rope_scaling;

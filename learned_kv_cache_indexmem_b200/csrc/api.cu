@@ -827,7 +827,7 @@ imem_status imem_set_rope(imem_ctx* h, const imem_rope* r) {
   const auto at = [&](double turns) {
     return r->rot_dim * log(r->orig_len / (tau * turns)) / (2 * log(r->base));
   };
-  const auto hold = [&](double x) { return fmin(fmax(x, 0.0), half - 1.0); };
+  const auto hold = [&](double x) { return fmin(fmax(x, 0.0), r->rot_dim - 1.0); };
   for (int i = 0; i < half; ++i) {
     const double theta = pow(r->base, -2.0 * i / r->rot_dim);
     double keep = 1.0;

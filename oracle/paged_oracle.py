@@ -26,8 +26,8 @@ def frequencies(rot, base=10000.0, scaling="plain", factor=1.0, low=1.0, high=4.
             w = min(1.0, max(0.0, (turns - low) / (high - low)))
         else:
             x = lambda n: rot * math.log(orig_len / (2 * math.pi * n)) / (2 * math.log(base))
-            a = min(max(math.floor(x(high)), 0), rot // 2 - 1)
-            b = min(max(math.ceil(x(low)), 0), rot // 2 - 1)
+            a = min(max(math.floor(x(high)), 0), rot - 1)
+            b = min(max(math.ceil(x(low)), 0), rot - 1)
             w = 1.0 - min(1.0, max(0.0, (i - a) / max(b - a, 1e-3)))
         out.append(theta * (w + (1 - w) / factor))
     return np.array(out)

@@ -154,6 +154,19 @@ def test_rotate(cuda_device, dtype, d, rot, layout, scaling):
     lay.close()
 
 
+@pytest.mark.parametrize("rot,orig_len", [(128, 131072), (64, 65536), (128, 1 << 24), (32, 100)])
+def test_ramp_borders(cuda_device, rot, orig_len):
+    """Ramps that end past the last pair, or before the first."""
+    kw = dict(base=10000.0, scaling="ramp", factor=16.0, low=1.0, high=32.0, orig_len=orig_len)
+    lay = layer(cuda_device, d=128, dtype="fp32", rot_dim=rot, layout="half", **kw)
+    bt = batch(cuda_device, [300], [300], d=128, dtype="fp32")
+    pos = np.random.default_rng(rot).integers(0, 1 << 20, 300).astype(np.int32)
+    q, _ = lay.rotate(bt.q, None, torch.from_numpy(pos).to(cuda_device))
+    check_rotated(q, bt.q, pos, po.frequencies(rot, **kw), "half")
+    lay.sync()
+    lay.close()
+
+
 def test_far_positions_keep_their_angle(cuda_device):
     lay = layer(cuda_device, d=64, dtype="fp32", base=10000.0)
     pos = np.array([2 ** 31 - 1, -2 ** 31, 2 ** 24 + 1, 131071], dtype=np.int32)

@@ -70,6 +70,23 @@ def test_scalings_hand_worked():
     assert np.allclose(ramp[:21], p[:21]) and np.allclose(ramp[46:], p[46:] / 16) and ramp[30] < p[30]
 
 
+def test_ramp_past_the_last_pair_hand_worked():
+    """The upper border is an index of dimensions, not of pairs: base 10000, 128
+    dimensions, 131072 positions: from floor(64 ln(131072/(64 pi))/ln 1e4) = 45 to
+    ceil(64 ln(131072/(2 pi))/ln 1e4) = 70, so that pair 63 keeps 1 - 18/25."""
+    p = po.frequencies(128, 10000.0)
+    ramp = po.frequencies(128, 10000.0, "ramp", 16.0, 1.0, 32.0, 131072)
+    assert np.allclose(ramp[:46], p[:46], rtol=1e-14)
+    w = 1 - (np.arange(46, 64) - 45) / 25
+    assert np.allclose(ramp[46:], p[46:] * (w + (1 - w) / 16), rtol=1e-14)
+    # 64 dimensions, 65536 positions: 20 to 33, pair 31 keeps 1 - 11/13
+    p = po.frequencies(64, 10000.0)
+    ramp = po.frequencies(64, 10000.0, "ramp", 4.0, 1.0, 32.0, 65536)
+    w = 1 - (np.arange(21, 32) - 20) / 13
+    assert np.allclose(ramp[:21], p[:21], rtol=1e-14)
+    assert np.allclose(ramp[21:], p[21:] * (w + (1 - w) / 4), rtol=1e-14)
+
+
 def test_attend_against_sdpa():
     rng = np.random.default_rng(3)
     Hq, Hkv, d, page = 4, 2, 8, 4
