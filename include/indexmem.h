@@ -463,8 +463,8 @@ imem_status imem_decode_online(imem_ctx* ctx, int batch, int B, const void* x_ne
  * new tokens has position kv_len[s] - n + i. A negative position (a sequence
  * padded in front) is padding too: it is not appended and attends to nothing.
  * Table entries past the last page that kv_len reaches are not read. A length
- * above max_pages * page_size (or 2^30), or an entry outside [0, n_pages) that a call
- * needs is reported by imem_sync as IMEM_ERR_RANGE (nothing out of bounds is
+ * below 0 or above max_pages * page_size (or 2^30) of a sequence with new tokens,
+ * or an entry outside [0, n_pages) that a call needs is reported by imem_sync as IMEM_ERR_RANGE (nothing out of bounds is
  * read or written; that sequence's results are unspecified). A tok_start that
  * descends or leaves [0, n_tokens] is reported likewise, every result of the
  * call is then unspecified. All tables and lengths are read on the device, in
@@ -563,7 +563,8 @@ imem_status imem_attend_paged(imem_ctx* ctx, int batch, int n_tokens, const int3
 /* Copies rows of the paged cache to contiguous arrays: K, V [batch, cap, Hkv, d],
  * K[s, i] = cached key at position idx[s * idx_stride + i], 0 <= i < n (n <= cap;
  * rows from n on are not written). idx = NULL: positions 0..n-1, those at or
- * past kv_len[s] skipped. An index outside [0, kv_len[s]) is reported as RANGE
+ * past kv_len[s] skipped. A length below 0 or above what the table holds is
+ * reported whatever is asked for. An index outside [0, kv_len[s]) is reported as RANGE
  * and its row not written. After gathering into a retained cache that decode
  * steps have used, call imem_decode_invalidate.
  * Errors: INVALID_ARG, SHAPE, ALIGN, CUDA; RANGE via imem_sync. */

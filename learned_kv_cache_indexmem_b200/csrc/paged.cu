@@ -30,9 +30,11 @@ gather_paged_kernel(const __grid_constant__ PagedView pg, int batch, int n,
   const int s = (int)(r / n), i = (int)(r - (long long)s * n);
   const int pos = idx ? idx[(long long)s * idx_stride + i] : i;
   const int len = pg.len[s];
-  const long long room = (long long)pg.max_pages << pg.page_log;
+  const long long room = min((long long)pg.max_pages << pg.page_log, 1LL << 30);
+  const bool bad = len < 0 || len > room;   // as seq_info
+  if (bad && i == 0 && lane == 0) record_error(err, DEV_RANGE);
   if (pos < 0 || pos >= len || pos >= room) {
-    if (lane == 0 && (idx || len > room)) record_error(err, DEV_RANGE);
+    if (lane == 0 && idx) record_error(err, DEV_RANGE);
     return;
   }
   const long long row = cache_row(pg, pg.table + (long long)s * pg.max_pages, pos);

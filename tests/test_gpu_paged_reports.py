@@ -20,6 +20,23 @@ def reported(lay):
     return None
 
 
+@pytest.mark.parametrize("idx", [True, False])
+@pytest.mark.parametrize("bad", [-1, -(1 << 31), "room", (1 << 30) + 1, (1 << 31) - 1])
+def test_gather_reports_lengths(cuda_device, idx, bad):
+    """A length below 0 or above what the table can hold is reported even where
+    every position asked for is inside; the other sequence's rows are copied."""
+    lay = layer(cuda_device)
+    bt = batch(cuda_device, [1, 1], [200, 120])
+    good, _ = lay.gather_paged(bt.cache, n=50)
+    assert reported(lay) is None
+    bt.cache.kv_len[0] = 16 * bt.cache.block_table.shape[1] + 1 if bad == "room" else bad
+    at = torch.arange(50, dtype=torch.int32, device=cuda_device).expand(2, 50).contiguous()
+    K, _ = lay.gather_paged(bt.cache, at if idx else None, n=50)
+    assert reported(lay) == "IMEM_ERR_RANGE"
+    assert torch.equal(K[1], good[1])
+    lay.close()
+
+
 @pytest.mark.parametrize("dtype,new", [("bf16", 1), ("bf16", 40), ("fp32", 1)])
 def test_attend_hints_above_the_longest_length(cuda_device, dtype, new):
     """Hints past the longest length a sequence may have (2^30) split the work as
