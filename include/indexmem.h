@@ -464,11 +464,11 @@ imem_status imem_decode_online(imem_ctx* ctx, int batch, int B, const void* x_ne
  * padded in front) is padding too: it is not appended and attends to nothing.
  * Table entries past the last page that kv_len reaches are not read. A length
  * below 0 or above max_pages * page_size (or 2^30) of a sequence with new tokens,
- * or an entry outside [0, n_pages) that a call needs is reported by imem_sync as IMEM_ERR_RANGE (nothing out of bounds is
- * read or written; that sequence's results are unspecified). A tok_start that
- * descends or leaves [0, n_tokens] is reported likewise, every result of the
- * call is then unspecified. All tables and lengths are read on the device, in
- * stream order. */
+ * or an entry outside [0, n_pages) that a call needs is reported by imem_sync as
+ * IMEM_ERR_RANGE (nothing out of bounds is read or written; that sequence's
+ * results are unspecified). A tok_start that descends or leaves [0, n_tokens] is
+ * reported likewise, every result of the call is then unspecified. All tables
+ * and lengths are read on the device, in stream order. */
 typedef struct {
   void* k;
   void* v;

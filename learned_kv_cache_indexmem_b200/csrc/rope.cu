@@ -126,6 +126,14 @@ rotate_kernel(const __grid_constant__ RotateArgs a, const __grid_constant__ Rope
   };
   if (tid < total) load(item(tid));
 
+  // ranges that no token falls into are looked at too, by the first CTA's warps
+  // without a token
+  if (kPaged && a.start && blockIdx.x == 0 && tid >= kRotTokens * 32)
+    for (int i = tid - kRotTokens * 32; i < a.batch; i += kRotThreads - kRotTokens * 32) {
+      const int from = a.start[i], to = a.start[i + 1];
+      if (from < 0 || to < from || to > a.n_tokens) record_error(err, DEV_RANGE);
+    }
+
   // positions and, for append, cache rows: one warp per token
   for (int k = tid >> 5; k < nt; k += kRotThreads / 32) {
     const int lane = tid & 31, t = t0 + k;

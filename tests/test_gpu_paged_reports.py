@@ -37,6 +37,20 @@ def test_gather_reports_lengths(cuda_device, idx, bad):
     lay.close()
 
 
+@pytest.mark.parametrize("start", [[0, 0, -1], [9, 9, 9], [0, 5, 3], [-1, 4, 8], [0, 4, 9], [5, 5, 0], [0, -5, 8]])
+def test_append_reports_token_ranges(cuda_device, start):
+    """Ranges that descend or leave [0, n_tokens], whether or not one of the
+    call's tokens falls into them."""
+    lay = layer(cuda_device)
+    bt = batch(cuda_device, [4, 4], [20, 40])
+    lay.append_paged(bt.k, bt.v, bt.cache, tok_start=bt.start)
+    assert reported(lay) is None
+    bad = torch.tensor(start, dtype=torch.int32, device=cuda_device)
+    lay.append_paged(bt.k, bt.v, bt.cache, tok_start=bad)
+    assert reported(lay) == "IMEM_ERR_RANGE"
+    lay.close()
+
+
 @pytest.mark.parametrize("dtype,new", [("bf16", 1), ("bf16", 40), ("fp32", 1)])
 def test_attend_hints_above_the_longest_length(cuda_device, dtype, new):
     """Hints past the longest length a sequence may have (2^30) split the work as
