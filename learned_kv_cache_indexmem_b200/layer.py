@@ -299,20 +299,20 @@ class IndexMemLayer:
                                                                        self._device))
 
     def _new(self, stream, shape, dtype):
-        """A tensor for the results of a call on ``stream``: memory of that stream
+        """A tensor for the results of a call on a given stream: memory of that stream
         (the current one's could still be written by work queued there), which
         the current one may read on."""
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self._device)
         caller = torch.cuda.current_stream(self._device)
         with self._as_current(stream):
             t = torch.empty(shape, dtype=dtype, device=self._device)
         t.record_stream(caller)
         return t
 
-    def _out(self, name: str, out, stream, n: int, heads: int):
+    def _out(self, name: str, out, like, stream, n: int, heads: int):
         """The output tensor (allocated if None) and its row stride."""
         if out is None:
+            if stream is None:
+                return torch.empty_like(like, memory_format=torch.contiguous_format), 0
             return self._new(stream, (n, heads, self._d), self.torch_dtype), 0
         return out, self._tokens(name, out, n, heads)
 
@@ -344,12 +344,12 @@ class IndexMemLayer:
             q_out = None
         else:
             qs = self._tokens("q", q, T, self._hq)
-            q_out, qos = self._out("q_out", q_out, stream, T, self._hq)
+            q_out, qos = self._out("q_out", q_out, q, stream, T, self._hq)
         if k is None:
             k_out = None
         else:
             ks = self._tokens("k", k, T, self._hkv)
-            k_out, kos = self._out("k_out", k_out, stream, T, self._hkv)
+            k_out, kos = self._out("k_out", k_out, k, stream, T, self._hkv)
         if T:
             B_.rotate(self.ctx, T, positions.data_ptr(), q if q is None else q.data_ptr(), qs,
                       q if q is None else q_out.data_ptr(), qos, k if k is None else k.data_ptr(),
@@ -374,7 +374,7 @@ class IndexMemLayer:
             q_out = None
         else:
             qs = self._tokens("q", q, T, self._hq)
-            q_out, qos = self._out("q_out", q_out, stream, T, self._hq)
+            q_out, qos = self._out("q_out", q_out, q, stream, T, self._hq)
         if T:
             B_.append_paged(self.ctx, b, T, tok_start if tok_start is None else tok_start.data_ptr(),
                             positions if positions is None else positions.data_ptr(), k.data_ptr(),
@@ -395,7 +395,7 @@ class IndexMemLayer:
         pg, b = self._paged(cache)
         T, Hq = q.shape[0], self._hq
         qs = self._tokens("q", q, T, Hq)
-        out, os_ = self._out("out", out, stream, T, Hq)
+        out, os_ = self._out("out", out, q, stream, T, Hq)
         if tok_start is not None:
             self._ints("tok_start", tok_start, (b + 1,))
         if lse is not None:
@@ -403,7 +403,8 @@ class IndexMemLayer:
                     not lse.is_contiguous() or lse.get_device() != self._index:
                 raise ValueError("lse must be contiguous float32 [%d, %d]" % (T, Hq))
         elif return_lse:
-            lse = self._new(stream, (T, Hq), torch.float32)
+            lse = (torch.empty(T, Hq, dtype=torch.float32, device=q.device) if stream is None
+                   else self._new(stream, (T, Hq), torch.float32))
         if scale is not None and not 1e-30 < scale < 1e30:
             raise ValueError("scale must be positive and finite")
         if max_new is None:
@@ -430,7 +431,10 @@ class IndexMemLayer:
             self._ints("idx", idx, (b, n))
         tail = (self._hkv, self._d)
         if K is None and V is None:
-            K, V = (self._new(stream, (b, n) + tail, self.torch_dtype) for _ in range(2))
+            if stream is None:
+                K, V = cache.K.new_empty((b, n) + tail), cache.K.new_empty((b, n) + tail)
+            else:
+                K, V = (self._new(stream, (b, n) + tail, self.torch_dtype) for _ in range(2))
         elif K is None or V is None or K.shape != V.shape or K.dim() != 4 or K.shape[0] != b or \
                 K.shape[1] < n or K.shape[2:] != tail or K.dtype != self.torch_dtype or \
                 V.dtype != self.torch_dtype or K.device != self._device or \
