@@ -939,7 +939,7 @@ imem_status imem_attend_paged(imem_ctx* h, int batch, int n_tokens, const int32_
   IMEM_CHECK(check_paged(cache, &a.pg));
   IMEM_CHECK(check_device(c));
   IMEM_CHECK(wait_pending(h->c, (cudaStream_t)stream));
-  if (!n_tokens || !max_new) return IMEM_OK;
+  if (!n_tokens) return IMEM_OK;   // max_new = 0 still reports sequences that have tokens
   a.batch = batch;
   a.n_tokens = n_tokens;
   a.max_new = max_new;

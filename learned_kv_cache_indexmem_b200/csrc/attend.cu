@@ -454,7 +454,7 @@ attend_f32_kernel(const __grid_constant__ AttendArgs a, int Hq, int G, int S, in
 template <int D, int KS>
 cudaError_t launch_f32(const Ctx& c, const AttendArgs& a, cudaStream_t st) {
   constexpr int BM = 64 / KS, kKeys = F32Cfg<D, KS>::keys, most = 16;
-  const int tiles = (a.max_new * c.group + BM - 1) / BM;
+  const int tiles = a.max_new ? (a.max_new * c.group + BM - 1) / BM : 1;   // 0: nothing but reports
   // CTAs that have rows, about; keys are split until four of them per SM, with
   // at least four stages each (one stage where the rows are few)
   const long long packed = ((long long)a.n_tokens * c.group + BM - 1) / BM;

@@ -51,6 +51,23 @@ def test_append_reports_token_ranges(cuda_device, start):
     lay.close()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attend_with_max_new_zero(cuda_device, dtype):
+    """max_new = 0 is right for a batch of padding alone; a sequence that has new
+    tokens is reported."""
+    lay = layer(cuda_device, dtype=dtype)
+    bt = batch(cuda_device, [0, 0], [20, 40], dtype=dtype, pad=4)
+    out, lse = torch.full_like(bt.q, 7.0), torch.full((4, 8), 7.0, device=cuda_device)
+    lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=0, out=out, lse=lse)
+    assert reported(lay) is None
+    assert (out == 7.0).all() and (lse == 7.0).all()
+    bt = batch(cuda_device, [3, 1], [20, 40], dtype=dtype)
+    lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=0, out=out, lse=lse)
+    assert reported(lay) == "IMEM_ERR_RANGE"
+    assert (out == 7.0).all() and (lse == 7.0).all()
+    lay.close()
+
+
 @pytest.mark.parametrize("dtype,new", [("bf16", 1), ("bf16", 40), ("fp32", 1)])
 def test_attend_hints_above_the_longest_length(cuda_device, dtype, new):
     """Hints past the longest length a sequence may have (2^30) split the work as
