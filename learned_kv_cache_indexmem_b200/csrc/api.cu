@@ -773,10 +773,10 @@ imem_status check_stride(const Ctx& c, int64_t* stride, int heads) {
   return (*stride * esize) % 16 ? IMEM_ERR_ALIGN : IMEM_OK;
 }
 
-// The 2^32 tokens' worth of grid and index arithmetic the kernels are written
-// for: batch and KV heads are grid dimensions, tokens * group stays an int.
-imem_status check_tokens(const Ctx& c, int batch, int n_tokens, const int32_t* tok_start) {
-  if (batch < 1 || batch > 65535 || c.cfg.n_kv_heads > 65535) return IMEM_ERR_SHAPE;
+// 2^24 tokens at most, so that query rows (tokens times a group of up to 8) and
+// their tiles stay ints. Grids are linear; each launcher checks its own.
+imem_status check_tokens(int batch, int n_tokens, const int32_t* tok_start) {
+  if (batch < 1 || batch > 65535) return IMEM_ERR_SHAPE;
   if (n_tokens < 0 || n_tokens > (1 << 24)) return IMEM_ERR_SHAPE;
   if (!tok_start) return n_tokens % batch ? IMEM_ERR_SHAPE : IMEM_OK;
   return aligned16(tok_start) ? IMEM_OK : IMEM_ERR_ALIGN;
@@ -856,7 +856,7 @@ imem_status imem_rotate(imem_ctx* h, int n_tokens, const int32_t* positions, con
   if (!h) return IMEM_ERR_INVALID_ARG;
   const Ctx& c = h->c;
   if (!c.rope.rot_dim || (!q && !k) || (inverse != 0 && inverse != 1)) return IMEM_ERR_INVALID_ARG;
-  IMEM_CHECK(check_tokens(c, 1, n_tokens, nullptr));
+  IMEM_CHECK(check_tokens(1, n_tokens, nullptr));
   IMEM_CHECK(check_ptr(positions));
   if (q) {
     IMEM_CHECK(check_ptr(q));
@@ -893,7 +893,7 @@ imem_status imem_append_paged(imem_ctx* h, int batch, int n_tokens, const int32_
   const Ctx& c = h->c;
   if (rotate != 0 && rotate != 1) return IMEM_ERR_INVALID_ARG;
   if (rotate && !c.rope.rot_dim) return IMEM_ERR_INVALID_ARG;
-  IMEM_CHECK(check_tokens(c, batch, n_tokens, tok_start));
+  IMEM_CHECK(check_tokens(batch, n_tokens, tok_start));
   if (positions) IMEM_CHECK(check_ptr(positions));
   IMEM_CHECK(check_ptr(k));
   IMEM_CHECK(check_ptr(v));
@@ -928,7 +928,7 @@ imem_status imem_attend_paged(imem_ctx* h, int batch, int n_tokens, const int32_
   if (!h) return IMEM_ERR_INVALID_ARG;
   const Ctx& c = h->c;
   if (!(scale >= 0.f) || isinf(scale)) return IMEM_ERR_INVALID_ARG;
-  IMEM_CHECK(check_tokens(c, batch, n_tokens, tok_start));
+  IMEM_CHECK(check_tokens(batch, n_tokens, tok_start));
   if (max_new < 0 || max_new > n_tokens || max_len < 0) return IMEM_ERR_SHAPE;
   IMEM_CHECK(check_ptr(q));
   IMEM_CHECK(check_ptr(out));

@@ -6,7 +6,8 @@
 // fp32 products on the tensor cores. A value is split into hi (rounded to the
 // operand format tf32, 11 significant bits) and lo = x - hi (exact, of either
 // sign; its upper 11 bits are kept), and a product becomes hi hi + hi lo +
-// lo hi with fp32 accumulation: what is dropped is below 2^-22 of |x y|. The
+// lo hi with fp32 accumulation: what is dropped is below 2^-21 of |x y| (lo lo
+// 2^-22, the bits of a lo behind its eleventh 2^-23 on either side). The
 // unit cuts its sums off instead of rounding them, which over many keys
 // would pull every sum towards zero, so that only short chains stay inside it
 // (16 dimensions, one stage of keys) and meet by rounded additions: 1.6e-6
@@ -14,7 +15,7 @@
 // MMA: one m16n8k8 (tf32) or m16n8k16 (bf16) per 16 clocks and SM quarter, so
 // three tf32 products cost as much as six bf16 ones of a three-way split with
 // less arithmetic around them, and both beat the fp32 units as far as shared
-// memory feeds those (1024 new tokens, 8 heads of 64: 44 us, 25 TFLOP/s; on
+// memory feeds those (1024 new tokens, 8 heads of 64: 44-47 us, 23-25 TFLOP/s; on
 // the fp32 units 56 us).
 //
 // An infinite value has no such halves (lo = inf - inf): its products are NaN

@@ -26,9 +26,19 @@
 // matters; value rows past the last key that any row sees are zeroed in
 // shared memory (0 * NaN would reach O).
 //
+// P is rounded to bf16 for the product with V, the type the tensor cores take
+// beside a bf16 V, as imem_decode does: 2^-8 of each weight at most, which over
+// many keys adds about as much to an output as its own rounding (error against
+// the exact outputs 0.0020-0.0022 of their size, 0.0017 from that alone). The
+// sum that divides is taken before the rounding. Leaving a maximum alone until
+// it has grown, and sharing exp2 out between two units (below), are published
+// techniques of attention kernels.
+//
 // Bound by the tensor cores and exp2 for long chunks (8192 new tokens at
-// 131072, 32 heads of 128: 14.1 ms, 1.21 PFLOP/s; four ragged prompts of up to
-// 4096: 357 us, 1.06 PFLOP/s), by HBM for a few tokens.
+// 131072, 32 heads of 128: 14.1-14.5 ms, 1.2 PFLOP/s; four ragged prompts of up to
+// 4096: 355 us, 1.07 PFLOP/s, on the same inputs again, 410-419 us, 0.92, on
+// others each time; 2048 tokens at 16384 keys, heads of 64: 359 us, 0.72), by HBM
+// for a few tokens.
 //
 // With too few tiles to fill the GPU the keys of a tile are split over a
 // cluster; the states (m, l, O) meet over distributed shared memory and are

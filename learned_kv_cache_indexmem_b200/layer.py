@@ -389,7 +389,8 @@ class IndexMemLayer:
         """Causal attention of the new tokens q [T, Hq, d] over the paged cache
         (their own rows appended before), out not overlapping q. scale: of the
         logits (default 1/sqrt(d)). max_new: most new tokens of a sequence
-        (default: T, or T / b without tok_start); max_len: the longest kv_len
+        (default: T, or T / b without tok_start; the kernel is chosen by it, so a
+        decode step with tok_start should say 1); max_len: the longest kv_len
         expected (a hint; default: what the table can hold). Returns out, or
         (out, lse [T, Hq] fp32) with return_lse."""
         pg, b = self._paged(cache)
