@@ -31,34 +31,35 @@ def definition(bt):
     out, lse = np.zeros((T, hq, d)), np.zeros((T, hq))
     spread, size = np.zeros((T, hq, d)), np.zeros((T, hq))
     finite = lambda x: np.where(np.isfinite(x), x, 0.0)
-    with np.errstate(invalid="ignore", over="ignore"):
+    with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
         for s, n in enumerate(bt.lens):
-            rows = po.slots(table[s], page, n)
+            rows, at = po.slots(table[s], page, n), slice(start[s], start[s + 1])
             k, v = K.reshape(-1, hkv, d)[rows], V.reshape(-1, hkv, d)[rows]
-            for t in range(start[s], start[s + 1]):
-                seen = n - (start[s + 1] - t) + 1
-                for h in range(hq):
-                    kk, vv = k[:seen, h // G], v[:seen, h // G]
-                    x = scale * (kk * q[t, h]).sum(1)
-                    size[t, h] = scale * (np.abs(finite(kk)) @ np.abs(q[t, h])).max()
-                    if np.isnan(x).any() or (x == np.inf).any():
-                        out[t, h] = np.nan
-                        lse[t, h] = np.nan if np.isnan(x).any() else np.inf
-                        continue
-                    if (x == -np.inf).all():
-                        out[t, h], lse[t, h] = 0.0, -np.inf
-                        continue
-                    p = np.exp(x - x.max())
-                    lse[t, h] = x.max() + np.log(p.sum())
-                    p /= p.sum()
-                    on = p > 0
-                    out[t, h] = (p[on, None] * vv[on]).sum(0)
-                    spread[t, h] = p @ np.abs(finite(vv))
+            new = start[s + 1] - start[s]
+            seen = np.arange(n)[None] <= (n - new + np.arange(new))[:, None]       # [token, key]
+            for h in range(hq):
+                kk, vv, qq = k[:, h // G], v[:, h // G], q[at, h]
+                x = scale * (qq[:, None] * kk).sum(2)
+                x[~seen] = -np.inf
+                size[at, h] = scale * np.where(seen, np.abs(qq) @ np.abs(finite(kk)).T, 0).max(1)
+                nan, inf, none = np.isnan(x).any(1), (x == np.inf).any(1), (x == -np.inf).all(1)
+                m = np.where(nan | inf | none, 0.0, x.max(1))
+                p = np.exp(x - m[:, None])
+                total = p.sum(1)
+                lse[at, h] = m + np.log(total)
+                p = np.where((nan | inf | none)[:, None], 0.0, p / total[:, None])
+                # a value counts where its weight is not 0
+                o = p @ finite(vv)
+                for j, e in zip(*np.nonzero(~np.isfinite(vv))):
+                    o[:, e] += np.where(p[:, j] > 0, vv[j, e], 0.0)
+                o[nan | inf] = np.nan
+                out[at, h], spread[at, h] = o, p @ np.abs(finite(vv))
+                lse[at, h] = np.where(nan, np.nan, np.where(inf, np.inf, np.where(none, -np.inf, lse[at, h])))
     return out, lse, spread, size
 
 
-def check(out, lse, bt):
-    ref, rl, spread, size = definition(bt)
+def check(out, lse, bt, defined):
+    ref, rl, spread, size = defined
     o, l = to_np(out), to_np(lse)
     d, n, e = o.shape[2], max(bt.lens), torch.finfo(out.dtype).eps / 2
     ds = 4 * U * (d + 4) * size
@@ -103,10 +104,11 @@ def test_non_finite_keys_and_values(cuda_device, dtype, d, new, kind):
             Kf[torch.from_numpy(rows).to(cuda_device), 0, 0] = float("-inf")
         else:
             Vf[at, 0, 5], Vf[at, 0, 6], Vf[at, 0, 7] = float("inf"), float("-inf"), float("nan")
+    defined = definition(bt)
     for hint in (None, 0):           # keys split over CTAs, and not
         out, lse = lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=new, max_len=hint, return_lse=True)
         lay.sync()
-        check(out, lse, bt)
+        check(out, lse, bt, defined)
     lay.close()
 
 
@@ -122,5 +124,5 @@ def test_fp32_values_of_later_tokens_stay_out(cuda_device, d, new):
         bt.cache.V.view(-1, 2, d)[at, s] = float("nan")
     out, lse = lay.attend_paged(bt.q, bt.cache, tok_start=bt.start, max_new=new, return_lse=True)
     lay.sync()
-    check(out, lse, bt)
+    check(out, lse, bt, definition(bt))
     lay.close()

@@ -132,3 +132,30 @@ def test_outputs_belong_to_the_stream_of_the_call(cuda_device):
             assert torch.equal(a, b)
         del over, copies
     lay.close()
+
+
+def test_evict_paged_in_a_graph(cuda_device):
+    """Captured after a first call, replayed after other keys went into the pages."""
+    L, Bg = 320, 48
+    lay, pages, x = _prompt(cuda_device, L)
+    st = lay.new_state(2, L, Bg, Bg, cuda_device)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        lay.evict_paged(x["X"], x["Q"], pages, st, Bg, chunk=64)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            lay.evict_paged(x["X"], x["Q"], pages, st, Bg, chunk=64)
+        lay.append_paged(x["V"].flatten(0, 1), x["K"].flatten(0, 1), pages)
+        x["X"].mul_(-0.5)
+        st.M.zero_(), st.bstab.zero_()
+        graph.replay()
+        got = _states(st)
+        st.M.zero_(), st.bstab.zero_()
+        lay.evict_paged(x["X"], x["Q"], pages, st, Bg, chunk=64)
+    stream.synchronize()
+    lay.sync()
+    for a, b in zip(got, _states(st)):
+        assert torch.equal(a, b)
+    del graph
+    lay.close()
